@@ -10,14 +10,18 @@
 #include <string>
 
 #include "../../include/flashcart.h"
+#include "fc_attn.h"
 #include "fc_conv.h"
+#include "fc_embed.h"
 #include "fc_graph.h"
 #include "fc_block.h"
 #include "fc_ladder.h"
 #include "fc_norm.h"
+#include "fc_qk_rope.h"
 #include "fc_radial.h"
 #include "fc_model.h"
 #include "fc_gemm.h"
+#include "fc_reduce.h"
 
 // Scratch of the allocation-free VJP (fc_edge_conv_vjp_noalloc): the VJP
 // workspace of one call, in device memory the library owns.  Each GPU the
@@ -27,6 +31,11 @@ constexpr size_t kNoAllocScratchBytes = FC_NOALLOC_SCRATCH_BYTES;
 static __device__ __align__(256) unsigned char scratch[kNoAllocScratchBytes];
 
 namespace {
+
+// bounds of the embedding, query/key norm and attention calls: what their
+// kernels count in 32 bits stays below 2^31
+constexpr int kMaxRows = 1 << 30;
+constexpr int kMaxHeads = 1024;
 
 thread_local std::string g_msg;
 
@@ -270,6 +279,158 @@ fc_status check_norm(const fc_norm_desc* d) {
   if (d->l_max > fc::kNormMaxRank) return fail(FC_ERR_UNSUPPORTED, "norm: l_max above 5 is not supported");
   if (!(d->eps >= 0.f) || !std::isfinite(d->eps))
     return fail(FC_ERR_INVALID_ARGUMENT, "norm: eps must be >= 0 and finite");
+  return FC_OK;
+}
+
+fc_status check_dtype(const char* what, fc_dtype t) {
+  if (t != FC_F32 && t != FC_BF16)
+    return fail(FC_ERR_UNSUPPORTED, "%s: dtype %d (FC_F32 and FC_BF16 are defined)", what, t);
+  return FC_OK;
+}
+
+fc_status check_embed(const fc_embed_desc* d) {
+  if (!d) return fail(FC_ERR_INVALID_ARGUMENT, "embedding descriptor is NULL");
+  if (d->n_tokens < 0) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: n_tokens must be >= 0 (got %d)", d->n_tokens);
+  if (d->n_rows < 1) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: n_rows must be >= 1 (got %d)", d->n_rows);
+  if (d->channels < 1) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: channels must be >= 1 (got %d)", d->channels);
+  if (d->n_tokens > kMaxRows || d->n_rows > kMaxRows || d->channels > kMaxRows)
+    return fail(FC_ERR_UNSUPPORTED, "embedding: counts above %d are not supported", kMaxRows);
+  if (!std::isfinite(d->scale)) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: scale must be finite");
+  return check_dtype("embedding", d->dtype);
+}
+
+fc_status check_qk(const fc_qk_rope_desc* d) {
+  if (!d) return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm descriptor is NULL");
+  if (d->n_nodes < 0) return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: n_nodes must be >= 0 (got %d)", d->n_nodes);
+  if (d->heads_q < 1 || d->heads_k < 0)
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: need heads_q >= 1 and heads_k >= 0");
+  if (d->head_dim < 2 || d->head_dim % 2 != 0)
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: head_dim must be even and >= 2 (got %d)", d->head_dim);
+  if (d->head_dim > fc::kQkMaxDim)
+    return fail(FC_ERR_UNSUPPORTED, "query/key norm: head_dim above %d is not supported", fc::kQkMaxDim);
+  if (d->heads_q > kMaxHeads || d->heads_k > kMaxHeads || d->n_nodes > kMaxRows)
+    return fail(FC_ERR_UNSUPPORTED, "query/key norm: more than %d heads or %d nodes are not supported", kMaxHeads,
+                kMaxRows);
+  if (d->n_freq < 0 || d->n_freq > d->head_dim / 2)
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: n_freq must be in [0, head_dim / 2] (got %d)", d->n_freq);
+  if (d->q_stride != 0 && d->q_stride < d->heads_q * d->head_dim)
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: q_stride %d is shorter than a row", d->q_stride);
+  if (d->k_stride != 0 && d->k_stride < d->heads_k * d->head_dim)
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: k_stride %d is shorter than a row", d->k_stride);
+  if (!(d->eps > 0.f) || !std::isfinite(d->eps))
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: eps must be > 0 and finite");
+  if ((d->flags & ~FC_ROPE_INTERLEAVED) != 0)
+    return fail(FC_ERR_UNSUPPORTED, "query/key norm: unknown flags 0x%x (FC_ROPE_INTERLEAVED is defined)", d->flags);
+  return check_dtype("query/key norm", d->dtype);
+}
+
+fc::QkRopeArgs qk_args(const fc_qk_rope_desc* d, const void* q, const void* k, const float* gamma_q,
+                       const float* gamma_k, const float* pos, const float* freq) {
+  fc::QkRopeArgs a{};
+  a.N = d->n_nodes, a.hq = d->heads_q, a.hk = d->heads_k, a.D = d->head_dim, a.R = d->n_freq;
+  a.qs = d->q_stride ? d->q_stride : d->heads_q * d->head_dim;
+  a.ks = d->k_stride ? d->k_stride : d->heads_k * d->head_dim;
+  a.eps = d->eps;
+  a.bf16 = d->dtype == FC_BF16;
+  a.interleaved = (d->flags & FC_ROPE_INTERLEAVED) != 0;
+  a.q = q, a.k = k, a.gamma_q = gamma_q, a.gamma_k = gamma_k, a.pos = pos, a.freq = freq;
+  return a;
+}
+
+// arrays common to both directions
+fc_status check_qk_arrays(const char* what, const fc_qk_rope_desc* d, const void* q, const void* k,
+                          const float* gamma_q, const float* gamma_k, const float* pos, const float* freq) {
+  const size_t e = d->dtype == FC_BF16 ? 2 : 4;
+  if (d->n_nodes > 0 && (!q || (d->heads_k > 0 && !k))) return fail(FC_ERR_INVALID_ARGUMENT, "%s: NULL q or k", what);
+  if ((d->n_nodes > 0 && d->n_freq > 0 && !pos != !freq) || (freq && !pos && d->n_nodes > 0))
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: pos and freq come together", what);
+  if (misaligned(q, e) || misaligned(k, e) || misaligned(gamma_q, 4) || misaligned(gamma_k, 4) || misaligned(pos, 4) ||
+      misaligned(freq, 4))
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: arrays must be aligned to their elements", what);
+  return FC_OK;
+}
+
+fc_status check_attn(const fc_attn_desc* d) {
+  if (!d) return fail(FC_ERR_INVALID_ARGUMENT, "attention descriptor is NULL");
+  if (d->n_query < 0 || d->n_key < 0) return fail(FC_ERR_INVALID_ARGUMENT, "attention: n_query and n_key must be >= 0");
+  if (d->n_segments < 1) return fail(FC_ERR_INVALID_ARGUMENT, "attention: n_segments must be >= 1 (got %d)", d->n_segments);
+  if (d->heads_k < 1 || d->heads_q < 1 || d->heads_q % d->heads_k != 0)
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention: heads_q must be a multiple of heads_k >= 1 (got %d, %d)",
+                d->heads_q, d->heads_k);
+  if (d->heads_q > fc::kAttnMaxHeads)
+    return fail(FC_ERR_UNSUPPORTED, "attention: more than %d heads are not supported", fc::kAttnMaxHeads);
+  if (d->head_dim < 1) return fail(FC_ERR_INVALID_ARGUMENT, "attention: head_dim must be >= 1");
+  if (d->head_dim % 8 != 0 || d->head_dim > fc::kAttnMaxDim)
+    return fail(FC_ERR_UNSUPPORTED, "attention: head_dim must be a multiple of 8 up to %d (got %d)", fc::kAttnMaxDim,
+                d->head_dim);
+  if (!(d->scale > 0.f) || !std::isfinite(d->scale))
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention: scale must be > 0 and finite");
+  if (!(d->cap >= 0.f) || !std::isfinite(d->cap))
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention: cap must be >= 0 and finite");
+  if ((d->flags & ~FC_ATTN_CAUSAL) != 0)
+    return fail(FC_ERR_UNSUPPORTED, "attention: unknown flags 0x%x (FC_ATTN_CAUSAL is defined)", d->flags);
+  // packed rows (row, shared head) and tiles are counted in 32 bits, threads
+  // of a launch too
+  const int64_t packed = (int64_t)d->n_query * (d->heads_q / d->heads_k);
+  if (packed > kMaxRows || d->n_key > kMaxRows || d->n_segments > kMaxRows / 64 ||
+      (std::max<int64_t>(packed, d->n_key) / 32 + d->n_segments) * d->heads_k > (int64_t(1) << 28))
+    return fail(FC_ERR_UNSUPPORTED, "attention: too many rows (n_query heads_q / heads_k and n_key up to %d)", kMaxRows);
+  const int piece = d->dtype == FC_BF16 ? 8 : 4;
+  const int rows[3] = {d->heads_q * d->head_dim, d->heads_k * d->head_dim, d->heads_k * d->head_dim};
+  const int32_t strides[3] = {d->q_stride, d->k_stride, d->v_stride};
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] != 0 && (strides[i] < rows[i] || strides[i] % piece != 0))
+      return fail(FC_ERR_INVALID_ARGUMENT,
+                  "attention: %c_stride %d is shorter than a row or not a whole number of 16-byte pieces", "qkv"[i],
+                  strides[i]);
+  return check_dtype("attention", d->dtype);
+}
+
+fc::AttnArgs attn_args(const fc_attn_desc* d, const fc_segments* seg, const void* q, const void* k, const void* v,
+                       const float* slope, const float* pos_q, const float* pos_k) {
+  fc::AttnArgs a{};
+  a.nq = d->n_query, a.nk = d->n_key, a.S = d->n_segments;
+  a.hq = d->heads_q, a.hk = d->heads_k, a.G = d->heads_q / d->heads_k, a.D = d->head_dim;
+  a.qs = d->q_stride ? d->q_stride : a.hq * a.D;
+  a.ks = d->k_stride ? d->k_stride : a.hk * a.D;
+  a.vs = d->v_stride ? d->v_stride : a.hk * a.D;
+  a.scale = d->scale, a.cap = d->cap;
+  a.causal = (d->flags & FC_ATTN_CAUSAL) != 0;
+  if (seg) {
+    a.seg_q = seg->q;
+    a.seg_k = seg->k ? seg->k : seg->q;
+    a.prefix = seg->prefix;
+  }
+  a.q = q, a.k = k, a.v = v;
+  if (slope) {
+    a.slope = slope, a.pos_q = pos_q;
+    a.self_pos = !pos_k && d->n_key > 0;   // an empty array may be NULL too
+    a.pos_k = pos_k ? pos_k : pos_q;
+  }
+  return a;
+}
+
+// arguments common to both directions
+fc_status check_attn_arrays(const char* what, const fc_attn_desc* d, const fc_segments* seg, const void* q,
+                            const void* k, const void* v, const float* slope, const float* pos_q, const float* pos_k) {
+  if ((!seg || !seg->q) && d->n_segments != 1)
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: %d segments need their offsets", what, d->n_segments);
+  if (seg && !seg->q && seg->k) return fail(FC_ERR_INVALID_ARGUMENT, "%s: key offsets without query offsets", what);
+  if (seg && seg->q && !seg->k && d->n_key != d->n_query)
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: shared offsets need n_key = n_query", what);
+  if (seg && seg->prefix && !(d->flags & FC_ATTN_CAUSAL))
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: a prefix needs FC_ATTN_CAUSAL", what);
+  if ((d->n_query > 0 && !q) || (d->n_key > 0 && (!k || !v)))
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: NULL q, k or v", what);
+  if (!slope && (pos_q || pos_k)) return fail(FC_ERR_INVALID_ARGUMENT, "%s: positions without slope", what);
+  if (slope && d->n_query > 0 && !pos_q) return fail(FC_ERR_INVALID_ARGUMENT, "%s: slope without pos_q", what);
+  if (slope && !pos_k && d->n_key > 0 && (d->n_key != d->n_query || (seg && seg->k)))
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: pos_k may be NULL only where keys and queries share rows and offsets", what);
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16))
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: q, k and v must be 16-byte aligned", what);
+  if (misaligned(slope, 4) || misaligned(pos_q, 4) || misaligned(pos_k, 4) ||
+      (seg && (misaligned(seg->q, 4) || misaligned(seg->k, 4) || misaligned(seg->prefix, 4))))
+    return fail(FC_ERR_INVALID_ARGUMENT, "%s: arrays must be 4-byte aligned", what);
   return FC_OK;
 }
 
@@ -1139,6 +1300,171 @@ fc_status fc_message_block_energy_forces(const fc_conv_desc* cd, const fc_graph*
   }
   mlp_conv_vjp(cd, g, pos, shift, hb, W + L.w_mlp, a, nullptr, forces, nullptr, mws, wb + L.cws, true, stream);
   return check_launch("message block energy/forces");
+}
+
+// ------------------------------------------- embedding, queries/keys, attention
+
+fc_status fc_embed_fwd(const fc_embed_desc* d, const void* table, const int32_t* ids, void* out, hipStream_t stream) {
+  if (fc_status s = check_embed(d)) return s;
+  if (d->n_tokens == 0) return ok();
+  if (!table || !ids || !out) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: NULL table, ids or out");
+  const size_t e = d->dtype == FC_BF16 ? 2 : 4;
+  if (misaligned(table, e) || misaligned(ids, 4) || misaligned(out, e))
+    return fail(FC_ERR_INVALID_ARGUMENT, "embedding: arrays must be aligned to their elements");
+  fc::launch_embed_fwd(d->n_tokens, d->n_rows, d->channels, d->dtype == FC_BF16,
+                       !misaligned(table, 16) && !misaligned(out, 16), d->scale, table, ids, out, stream);
+  return check_launch("embedding forward");
+}
+
+size_t fc_embed_workspace_bytes(const fc_embed_desc* d) {
+  if (check_embed(d) != FC_OK || d->n_tokens == 0) return 0;
+  auto bytes = [&](bool aligned) {
+    return fc::embed_plan(d->n_tokens, d->n_rows, d->channels, d->dtype == FC_BF16, aligned, nullptr).bytes;
+  };
+  return std::max(bytes(true), bytes(false));
+}
+
+fc_status fc_embed_vjp(const fc_embed_desc* d, const int32_t* ids, const void* g_out, float* table_grad,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (fc_status s = check_embed(d)) return s;
+  if (!table_grad || (d->n_tokens > 0 && (!ids || !g_out)))
+    return fail(FC_ERR_INVALID_ARGUMENT, "embedding VJP: NULL ids, g_out or table_grad");
+  const size_t e = d->dtype == FC_BF16 ? 2 : 4;
+  if (misaligned(ids, 4) || misaligned(g_out, e) || misaligned(table_grad, 4))
+    return fail(FC_ERR_INVALID_ARGUMENT, "embedding VJP: arrays must be aligned to their elements");
+  if (d->n_tokens == 0) {
+    fc::launch_zero((size_t)d->n_rows * d->channels, table_grad, stream);
+    return check_launch("embedding VJP");
+  }
+  const size_t need = fc_embed_workspace_bytes(d);
+  if (!workspace || workspace_bytes < need || misaligned(workspace, 256))
+    return fail(FC_ERR_WORKSPACE, "embedding VJP needs %zu workspace bytes, 256-byte aligned", need);
+  const bool aligned = !misaligned(g_out, 16) && !misaligned(table_grad, 16);
+  const fc::EmbedPlan p =
+      fc::embed_plan(d->n_tokens, d->n_rows, d->channels, d->dtype == FC_BF16, aligned, workspace);
+  fc::launch_embed_vjp(p, d->dtype == FC_BF16, d->scale, ids, g_out, table_grad, stream);
+  return check_launch("embedding VJP");
+}
+
+fc_status fc_qk_norm_rope_fwd(const fc_qk_rope_desc* d, const void* q, const void* k, const float* gamma_q,
+                              const float* gamma_k, const float* pos, const float* freq, void* q_out, void* k_out,
+                              hipStream_t stream) {
+  if (fc_status s = check_qk(d)) return s;
+  if (fc_status s = check_qk_arrays("query/key norm", d, q, k, gamma_q, gamma_k, pos, freq)) return s;
+  if (d->n_nodes == 0) return ok();
+  if (!q_out || (d->heads_k > 0 && !k_out)) return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: NULL q_out or k_out");
+  const size_t e = d->dtype == FC_BF16 ? 2 : 4;
+  if (misaligned(q_out, e) || misaligned(k_out, e))
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: arrays must be aligned to their elements");
+  fc::QkRopeArgs a = qk_args(d, q, k, gamma_q, gamma_k, pos, freq);
+  a.q_out = q_out, a.k_out = k_out;
+  fc::launch_qk_rope_fwd(a, stream);
+  return check_launch("query/key norm forward");
+}
+
+size_t fc_qk_norm_rope_workspace_bytes(const fc_qk_rope_desc* d) {
+  if (check_qk(d) != FC_OK) return 0;
+  const fc::QkRopeArgs a = qk_args(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return (size_t)fc::qk_rope_vjp_blocks(a) * 2 * d->head_dim * sizeof(float);
+}
+
+fc_status fc_qk_norm_rope_vjp(const fc_qk_rope_desc* d, const void* q, const void* k, const float* gamma_q,
+                              const float* gamma_k, const float* pos, const float* freq, const void* g_q,
+                              const void* g_k, void* q_grad, void* k_grad, float* gamma_q_grad, float* gamma_k_grad,
+                              float* pos_grad, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (fc_status s = check_qk(d)) return s;
+  if (fc_status s = check_qk_arrays("query/key norm VJP", d, q, k, gamma_q, gamma_k, pos, freq)) return s;
+  const bool keys = d->heads_k > 0;
+  if (d->n_nodes > 0 && (!g_q || (keys && !g_k)))
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm VJP: NULL g_q or g_k");
+  if (!q_grad && !k_grad && !gamma_q_grad && !gamma_k_grad && !pos_grad && d->n_nodes > 0)
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm VJP: no output requested");
+  if (pos_grad && d->n_nodes > 0 && !pos)
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm VJP: pos_grad without pos");
+  const size_t e = d->dtype == FC_BF16 ? 2 : 4;
+  if (misaligned(g_q, e) || misaligned(g_k, e) || misaligned(q_grad, e) || misaligned(k_grad, e) ||
+      misaligned(gamma_q_grad, 4) || misaligned(gamma_k_grad, 4) || misaligned(pos_grad, 4) || misaligned(workspace, 16))
+    return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm VJP: arrays must be aligned to their elements");
+  if (d->n_nodes == 0) {
+    if (gamma_q_grad) fc::launch_zero(d->head_dim, gamma_q_grad, stream);
+    if (gamma_k_grad) fc::launch_zero(d->head_dim, gamma_k_grad, stream);
+    return check_launch("query/key norm VJP");
+  }
+  const size_t need = fc_qk_norm_rope_workspace_bytes(d);
+  const bool sums = gamma_q_grad || gamma_k_grad;
+  if (sums && (!workspace || workspace_bytes < need))
+    return fail(FC_ERR_WORKSPACE, "query/key norm VJP needs %zu workspace bytes for gamma gradients", need);
+  fc::QkRopeArgs a = qk_args(d, q, k, gamma_q, gamma_k, pos, freq);
+  a.g_q = g_q, a.g_k = g_k, a.q_grad = q_grad, a.k_grad = k_grad, a.pos_grad = pos_grad;
+  a.part = sums ? static_cast<float*>(workspace) : nullptr;
+  fc::launch_qk_rope_vjp(a, gamma_q_grad, gamma_k_grad, stream);
+  return check_launch("query/key norm VJP");
+}
+
+fc_status fc_segments_validate(int32_t n_segments, int32_t n_rows, const int32_t* offsets) {
+  if (n_segments < 1 || n_rows < 0) return fail(FC_ERR_INVALID_ARGUMENT, "need n_segments >= 1, n_rows >= 0");
+  if (!offsets) return fail(FC_ERR_INVALID_ARGUMENT, "NULL offsets");
+  if (offsets[0] != 0) return fail(FC_ERR_INVALID_ARGUMENT, "offsets[0] = %d, expected 0", offsets[0]);
+  for (int s = 0; s < n_segments; ++s)
+    if (offsets[s + 1] < offsets[s]) return fail(FC_ERR_INVALID_ARGUMENT, "offsets decrease at segment %d", s);
+  if (offsets[n_segments] > n_rows)
+    return fail(FC_ERR_INVALID_ARGUMENT, "offsets end at %d, beyond %d rows", offsets[n_segments], n_rows);
+  return ok();
+}
+
+size_t fc_attention_workspace_bytes(const fc_attn_desc* d, int32_t op) {
+  if (check_attn(d) != FC_OK || op < 0 || op > 1) return 0;
+  const fc::AttnArgs a = attn_args(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return fc::attn_workspace_bytes(a, d->dtype == FC_BF16, op);
+}
+
+fc_status fc_attention_fwd(const fc_attn_desc* d, const fc_segments* seg, const void* q, const void* k, const void* v,
+                           const float* slope, const float* pos_q, const float* pos_k, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (fc_status s = check_attn(d)) return s;
+  if (fc_status s = check_attn_arrays("attention", d, seg, q, k, v, slope, pos_q, pos_k)) return s;
+  if (d->n_query == 0) return ok();
+  if (!out || !lse) return fail(FC_ERR_INVALID_ARGUMENT, "attention: NULL out or lse");
+  if (misaligned(out, 16) || misaligned(lse, 4))
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention: out must be 16-byte aligned, lse 4-byte aligned");
+  const size_t need = fc_attention_workspace_bytes(d, 0);
+  if (need > 0 && (!workspace || workspace_bytes < need || misaligned(workspace, 256)))
+    return fail(FC_ERR_WORKSPACE, "attention needs %zu workspace bytes, 256-byte aligned", need);
+  fc::AttnArgs a = attn_args(d, seg, q, k, v, slope, pos_q, pos_k);
+  a.out = out, a.lse = lse;
+  fc::launch_attn_fwd(a, d->dtype == FC_BF16, workspace, stream);
+  return check_launch("attention forward");
+}
+
+fc_status fc_attention_vjp(const fc_attn_desc* d, const fc_segments* seg, const void* q, const void* k, const void* v,
+                           const float* slope, const float* pos_q, const float* pos_k, const void* out,
+                           const float* lse, const void* g_out, void* q_grad, void* k_grad, void* v_grad,
+                           float* slope_grad, float* pos_q_grad, float* pos_k_grad, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  if (fc_status s = check_attn(d)) return s;
+  if (fc_status s = check_attn_arrays("attention VJP", d, seg, q, k, v, slope, pos_q, pos_k)) return s;
+  if (d->n_query > 0 && (!out || !lse || !g_out))
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention VJP: NULL out, lse or g_out");
+  if (!q_grad && !k_grad && !v_grad && !slope_grad && !pos_q_grad && !pos_k_grad && (d->n_query > 0 || d->n_key > 0))
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention VJP: no output requested");
+  if (!slope && (slope_grad || pos_q_grad || pos_k_grad))
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention VJP: slope or position gradient without slope");
+  if (pos_k_grad && !pos_k && d->n_key > 0)
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention VJP: without pos_k the gradient is whole in pos_q_grad");
+  if (misaligned(out, 16) || misaligned(g_out, 16) || misaligned(q_grad, 16) || misaligned(k_grad, 16) ||
+      misaligned(v_grad, 16))
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention VJP: out, g_out, q_grad, k_grad and v_grad must be 16-byte aligned");
+  if (misaligned(lse, 4) || misaligned(slope_grad, 4) || misaligned(pos_q_grad, 4) || misaligned(pos_k_grad, 4))
+    return fail(FC_ERR_INVALID_ARGUMENT, "attention VJP: arrays must be 4-byte aligned");
+  const size_t need = fc_attention_workspace_bytes(d, 1);
+  if (need > 0 && (!workspace || workspace_bytes < need || misaligned(workspace, 256)))
+    return fail(FC_ERR_WORKSPACE, "attention VJP needs %zu workspace bytes, 256-byte aligned", need);
+  fc::AttnArgs a = attn_args(d, seg, q, k, v, slope, pos_q, pos_k);
+  a.out = const_cast<void*>(out), a.lse = const_cast<float*>(lse), a.g = g_out;
+  a.gq = q_grad, a.gk = k_grad, a.gv = v_grad;
+  a.g_slope = slope_grad, a.g_pos_q = pos_q_grad, a.g_pos_k = pos_k_grad;
+  fc::launch_attn_vjp(a, d->dtype == FC_BF16, workspace, stream);
+  return check_launch("attention VJP");
 }
 
 }  // extern "C"

@@ -1,0 +1,297 @@
+// Attention among the rows of each segment: how a call is cut into launches,
+// and the reductions around the kernels of fc_attn_kernels.h.
+//
+// Splitting.  A column tile walks its whole row axis in one block when there
+// are enough columns for the chip.  With few columns (single queries over
+// many atoms) the walked axis is cut into `splits` parts, whose partial
+// results go to the workspace and are joined in split order.
+#include "fc_attn.h"
+
+#include <algorithm>
+
+#include "fc_reduce.h"
+#include "fc_types.h"
+
+namespace fc {
+namespace {
+
+// rows that belong to a segment; the others are left as they are
+__device__ __forceinline__ bool in_segments(const int* off, int S, int n, int row) {
+  return !off || (row >= max(0, off[0]) && row < min(n, off[S]));
+}
+
+// out = sum_s w_s o_s with w_s = exp(lse_s - lse); four elements per thread
+template <class T>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnPart p) {
+  const int per = a.D / 4;
+  const size_t rows = (size_t)a.nq * a.hq, t = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t row = t / per;
+  const int d = (int)(t % per) * 4;
+  if (row >= rows || !in_segments(a.seg_q, a.S, a.nq, (int)(row / a.hq))) return;
+  float m = -__builtin_huge_valf();
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.lse[s * rows + row]);
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  if (m != -__builtin_huge_valf())
+    for (int s = 0; s < p.splits; ++s) {
+      const float w = __expf(p.lse[s * rows + row] - m);
+      float x[4];
+      load_f32<float, 4>(p.o + (s * rows + row) * a.D + d, x);
+      sum += w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(w, x[i], o[i]);
+    }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] *= inv;
+  store_f32<T, 4>(static_cast<T*>(a.out) + row * a.D + d, o);
+  if (d == 0) a.lse[row] = sum > 0.f ? m + __logf(sum) : m;
+}
+
+// out[row][.] = sum_s part[s][row][.] for rows of `width` elements
+template <class T>
+__global__ __launch_bounds__(256) void attn_sum_kernel(int n, int width, int S, int splits, const int* seg,
+                                                       const float* __restrict__ part, T* __restrict__ out) {
+  const size_t t = (size_t)blockIdx.x * 256 + threadIdx.x, total = (size_t)n * width, at = t * 4;
+  if (at >= total || !in_segments(seg, S, n, (int)(at / width))) return;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) {
+    float y[4];
+    load_f32<float, 4>(part + s * total + at, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] += y[i];
+  }
+  store_f32<T, 4>(out + at, x);
+}
+
+// delta[row] = <out, g> of a query row and head; eight lanes per row
+template <class T>
+__global__ __launch_bounds__(256) void attn_dot_kernel(AttnArgs a, float* __restrict__ delta) {
+  const size_t rows = (size_t)a.nq * a.hq, row = ((size_t)blockIdx.x * 256 + threadIdx.x) / 8;
+  float s = 0.f;
+  if (row < rows) {
+    const T* o = static_cast<const T*>(a.out) + row * a.D;
+    const T* g = static_cast<const T*>(a.g) + row * a.D;
+    for (int d = (threadIdx.x % 8) * 4; d < a.D; d += 32) {
+      float x[4], y[4];
+      load_f32<T, 4>(o + d, x);
+      load_f32<T, 4>(g + d, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = fmaf(x[i], y[i], s);
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) s += __shfl_xor(s, o);
+  if (row < rows && threadIdx.x % 8 == 0) delta[row] = s;
+}
+
+// position gradient of a row: its heads and splits in order; `self` adds the
+// part it has as a key
+__global__ __launch_bounds__(256) void attn_pos_kernel(int n, int S, const int* seg, int h0, int s0,
+                                                       const float* __restrict__ p0, int h1, int s1,
+                                                       const float* __restrict__ p1, float* __restrict__ out) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n || !in_segments(seg, S, n, i)) return;
+  float x = 0.f, y = 0.f, z = 0.f;
+  auto add = [&](int H, int splits, const float* part) {
+    for (int s = 0; s < splits; ++s)
+      for (int h = 0; h < H; ++h) {
+        float v[4];
+        load_f32<float, 4>(part + (((size_t)s * n + i) * H + h) * 4, v);
+        x += v[0], y += v[1], z += v[2];
+      }
+  };
+  add(h0, s0, p0);
+  if (p1) add(h1, s1, p1);
+  out[3 * (size_t)i] = x, out[3 * (size_t)i + 1] = y, out[3 * (size_t)i + 2] = z;
+}
+
+// slope gradients: sums of a run of rows per block, [blocks][hq]; a thread
+// has one head and every y-th row of the run
+__global__ __launch_bounds__(256) void attn_slope_kernel(int n, int H, int S, const int* seg, int splits, int run,
+                                                         const float* __restrict__ part, float* __restrict__ out) {
+  __shared__ float lds[256];
+  const int h = threadIdx.x, lo = blockIdx.x * run, hi = min(n, lo + run);
+  float t = 0.f;
+  if (h < H)
+    for (int s = 0; s < splits; ++s)
+      for (int i = lo + threadIdx.y; i < hi; i += blockDim.y)
+        if (in_segments(seg, S, n, i)) t += part[(((size_t)s * n + i) * H + h) * 4 + 3];
+  lds[threadIdx.y * blockDim.x + h] = t;
+  __syncthreads();
+  if (threadIdx.y != 0 || h >= H) return;
+  t = 0.f;
+  for (int y = 0; y < (int)blockDim.y; ++y) t += lds[y * blockDim.x + h];
+  out[(size_t)blockIdx.x * H + h] = t;
+}
+
+// ------------------------------------------------------------------- plans --
+
+struct PassPlan {
+  int waves, splits;
+};
+
+// `cols` columns and `rows` walked rows in all, over S segments; `heads`
+// key heads.
+//  * Four waves share a row tile; where a segment's columns fill at most one
+//    and a half waves, a block is one wave.
+//  * The walk is split until the chip has two blocks (of four waves) per CU,
+//    in parts of 128 rows at least.
+PassPlan plan_pass(int64_t cols, int64_t rows, int S, int heads) {
+  PassPlan p;
+  const int64_t mean = (cols + S - 1) / S;
+  p.waves = mean <= 48 ? 1 : 4;
+  const int64_t tiles = std::max<int64_t>(1, (mean + 32 * p.waves - 1) / (32 * p.waves)) * S * heads;
+  const int64_t want = 512 * 4 / p.waves / tiles, most = rows / S / 128;
+  p.splits = (int)std::clamp<int64_t>(std::min(want, most), 1, 64);
+  return p;
+}
+
+struct Plan {
+  PassPlan fwd, query, key;
+  bool exact_delta;   // delta from the scores, not from the rounded out
+  int slope_run, slope_blocks;
+  AttnPart pf, pd, pq, pk;
+  float *row, *col, *slope;
+  size_t bytes;
+};
+
+Plan make_plan(const AttnArgs& a, bool is_bf16, int op, void* ws) {
+  Plan p{};
+  const int64_t cq = (int64_t)a.nq * a.G;
+  p.fwd = p.query = plan_pass(cq, a.nk, a.S, a.hk);
+  p.key = plan_pass(a.nk, cq, a.S, a.hk);
+  // Position and slope gradients are fp32 outputs; with delta from a
+  // bfloat16 out they would carry its rounding.
+  p.exact_delta = is_bf16 && a.slope && (a.g_slope || a.g_pos_q || a.g_pos_k);
+  size_t at = 0;
+  auto take = [&](size_t floats) {
+    float* q = reinterpret_cast<float*>(static_cast<char*>(ws) + at);
+    at += (floats * sizeof(float) + 255) / 256 * 256;
+    return q;
+  };
+  const size_t rq = (size_t)a.nq * a.hq, rk = (size_t)a.nk * a.hk;
+  if (op == 0) {
+    p.pf.splits = p.fwd.splits;
+    if (p.fwd.splits > 1) {
+      p.pf.o = take(p.fwd.splits * rq * a.D);
+      p.pf.lse = take(p.fwd.splits * rq);
+    }
+  } else {
+    AttnPart c{};
+    c.dsplits = p.exact_delta ? p.query.splits : 1;
+    c.delta = take(c.dsplits * rq);
+    if (a.slope) {
+      c.row = take(p.query.splits * rq * 4);
+      c.col = take(p.key.splits * rk * 4);
+      p.slope_run = std::clamp(a.nq / 1024, 16, 256);
+      p.slope_blocks = (a.nq + p.slope_run - 1) / p.slope_run;
+      p.slope = take((size_t)p.slope_blocks * a.hq);
+    }
+    const size_t nq = p.query.splits > 1 ? p.query.splits * rq * a.D : 0;
+    const size_t nk = p.key.splits > 1 ? p.key.splits * rk * a.D : 0;
+    // one after the other on the stream: the passes share this part
+    float* o = take(std::max(nq, 2 * nk));
+    p.pd = p.pq = p.pk = c;
+    p.pq.splits = p.query.splits, p.pq.o = o;
+    p.pk.splits = p.key.splits, p.pk.o = o, p.pk.o2 = o + nk;
+  }
+  p.bytes = at;
+  return p;
+}
+
+template <class T>
+void launch_dim(const AttnLaunch& l, const AttnArgs& a, const AttnPart& p, hipStream_t st) {
+  if (a.D <= 16)
+    attn_launch<T, 16>(l, a, p, st);
+  else if (a.D <= 32)
+    attn_launch<T, 32>(l, a, p, st);
+  else if (a.D <= 64)
+    attn_launch<T, 64>(l, a, p, st);
+  else
+    attn_launch<T, 128>(l, a, p, st);
+}
+
+void launch_pass(bool is_bf16, const AttnLaunch& l, const AttnArgs& a, const AttnPart& p, hipStream_t st) {
+  is_bf16 ? launch_dim<bf16>(l, a, p, st) : launch_dim<float>(l, a, p, st);
+}
+
+unsigned blocks_of(size_t threads) { return (unsigned)((threads + 255) / 256); }
+
+void sum_splits(bool is_bf16, int n, int width, int S, const int* seg, int splits, const float* part, void* out,
+                hipStream_t st) {
+  if (!out) return;
+  const dim3 g(blocks_of((size_t)n * width / 4));
+  if (is_bf16)
+    hipLaunchKernelGGL(attn_sum_kernel<bf16>, g, dim3(256), 0, st, n, width, S, splits, seg, part,
+                       static_cast<bf16*>(out));
+  else
+    hipLaunchKernelGGL(attn_sum_kernel<float>, g, dim3(256), 0, st, n, width, S, splits, seg, part,
+                       static_cast<float*>(out));
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(const AttnArgs& a, bool is_bf16, int op) {
+  // the largest a call of this descriptor can need: every gradient wanted
+  AttnArgs b = a;
+  static const float some = 0.f;
+  b.slope = &some;
+  b.g_slope = const_cast<float*>(&some);
+  return make_plan(b, is_bf16, op, nullptr).bytes;
+}
+
+void launch_attn_fwd(const AttnArgs& a, bool is_bf16, void* ws, hipStream_t st) {
+  if (a.nq == 0) return;
+  const Plan p = make_plan(a, is_bf16, 0, ws);
+  launch_pass(is_bf16, {kAttnFwd, p.fwd.waves}, a, p.pf, st);
+  if (p.fwd.splits == 1) return;
+  const dim3 g(blocks_of((size_t)a.nq * a.hq * (a.D / 4)));
+  if (is_bf16)
+    hipLaunchKernelGGL(attn_join_kernel<bf16>, g, dim3(256), 0, st, a, p.pf);
+  else
+    hipLaunchKernelGGL(attn_join_kernel<float>, g, dim3(256), 0, st, a, p.pf);
+}
+
+void launch_attn_vjp(const AttnArgs& a, bool is_bf16, void* ws, hipStream_t st) {
+  const Plan p = make_plan(a, is_bf16, 1, ws);
+  if (a.nq > 0) {
+    if (p.exact_delta) {
+      launch_pass(is_bf16, {kAttnDelta, p.query.waves}, a, p.pd, st);
+    } else {
+      const dim3 g(blocks_of((size_t)a.nq * a.hq * 8));
+      if (is_bf16)
+        hipLaunchKernelGGL(attn_dot_kernel<bf16>, g, dim3(256), 0, st, a, p.pd.delta);
+      else
+        hipLaunchKernelGGL(attn_dot_kernel<float>, g, dim3(256), 0, st, a, p.pd.delta);
+    }
+    if (a.gq || a.g_slope || a.g_pos_q) {
+      launch_pass(is_bf16, {kAttnQuery, p.query.waves}, a, p.pq, st);
+      if (p.query.splits > 1)
+        sum_splits(is_bf16, a.nq, a.hq * a.D, a.S, a.seg_q, p.query.splits, p.pq.o, a.gq, st);
+    }
+  }
+  if (a.nk > 0 && (a.gk || a.gv || a.g_pos_k || (a.g_pos_q && a.self_pos))) {
+    launch_pass(is_bf16, {kAttnKey, p.key.waves}, a, p.pk, st);
+    if (p.key.splits > 1) {
+      sum_splits(is_bf16, a.nk, a.hk * a.D, a.S, a.seg_k, p.key.splits, p.pk.o, a.gk, st);
+      sum_splits(is_bf16, a.nk, a.hk * a.D, a.S, a.seg_k, p.key.splits, p.pk.o2, a.gv, st);
+    }
+  }
+  if (a.g_pos_q && a.nq > 0)
+    hipLaunchKernelGGL(attn_pos_kernel, dim3(blocks_of(a.nq)), dim3(256), 0, st, a.nq, a.S, a.seg_q, a.hq,
+                       p.query.splits, p.pq.row, a.hk, p.key.splits, a.self_pos ? p.pk.col : nullptr, a.g_pos_q);
+  if (a.g_pos_k && a.nk > 0)
+    hipLaunchKernelGGL(attn_pos_kernel, dim3(blocks_of(a.nk)), dim3(256), 0, st, a.nk, a.S, a.seg_k, a.hk,
+                       p.key.splits, p.pk.col, 0, 0, nullptr, a.g_pos_k);
+  if (a.g_slope) {
+    if (a.nq > 0) {
+      int x = 1;
+      while (x < a.hq) x <<= 1;
+      hipLaunchKernelGGL(attn_slope_kernel, dim3(p.slope_blocks), dim3(x, 256 / x), 0, st, a.nq, a.hq, a.S, a.seg_q,
+                         p.query.splits, p.slope_run, p.pq.row, p.slope);
+    }
+    launch_block_sum(p.slope_blocks, a.hq, p.slope, a.g_slope, st);
+  }
+}
+
+}  // namespace fc

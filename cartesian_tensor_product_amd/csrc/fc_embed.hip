@@ -1,0 +1,423 @@
+// Scaled lookup of table rows (species, tokens) and its gradient for gfx950:
+//   out[n][c]  = scale table[id_n][c],
+//   grad[r][c] = scale sum_{n : id_n = r} g[n][c],
+// ids outside [0, R) are padding: a zero row, no gradient.
+//
+// Lookup: one 16-byte piece per lane; bound by the write of out.
+//
+// Gradient: sums over tokens of one row in a fixed order, without
+// floating-point atomics.  A stable radix sort of the ids gives the tokens of
+// each row as one run of the sorted order.  The order is cut into chunks of
+// equal length whatever the runs are, so that one very frequent row (a common
+// species) costs no more than many rare ones.  A group of lanes walks its
+// chunk, adds the tokens' rows in fp32 and writes a row when its run ends;
+// the runs cut by a chunk edge go to partial sums (at most two per chunk),
+// which the last kernel adds in chunk order.  That kernel also writes the
+// zeros of rows without a token.  Bound by the read of g.
+#include "fc_embed.h"
+
+#include <algorithm>
+
+#include "fc_types.h"
+
+namespace fc {
+namespace {
+
+constexpr int kSortThreads = 256, kSortRounds = 8, kSortItems = kSortThreads * kSortRounds;
+constexpr int kSortWaves = kSortThreads / 64;
+
+template <class T, int V>
+__global__ __launch_bounds__(256) void embed_fwd_kernel(int N, int R, int C, float scale, const T* __restrict__ table,
+                                                        const int* __restrict__ ids, T* __restrict__ out) {
+  const int n = blockIdx.x * blockDim.y + threadIdx.y;
+  if (n >= N) return;
+  const int id = ids[n];
+  const bool real = id >= 0 && id < R;
+  const T* src = table + (size_t)(real ? id : 0) * C;
+  T* dst = out + (size_t)n * C;
+  for (int c = threadIdx.x * V; c < C; c += blockDim.x * V) {
+    float x[V];
+    load_f32<T, V>(src + c, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = real ? x[i] * scale : 0.f;
+    store_f32<T, V>(dst + c, x);
+  }
+}
+
+// ---------------------------------------------------------------- the sort --
+
+// ids as sort keys: padding sorts behind the last row
+__device__ __forceinline__ int key_of(int id, int R) { return id >= 0 && id < R ? id : R; }
+
+// counts of one digit per block, hist[digit][block]; the first pass also
+// clears the run bounds of every row
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(int N, int R, int shift, int ndig, bool first_pass,
+                                                                  const int* __restrict__ keys,
+                                                                  int* __restrict__ hist, int* __restrict__ first,
+                                                                  int* __restrict__ last) {
+  __shared__ int cnt[256];
+  const int t = threadIdx.x;
+  cnt[t] = 0;
+  __syncthreads();
+  const int base = blockIdx.x * kSortItems;
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    const int n = base + i * kSortThreads + t;
+    if (n < N) {
+      const int k = first_pass ? key_of(keys[n], R) : keys[n];
+      atomicAdd(&cnt[(k >> shift) & (ndig - 1)], 1);   // integer counts: no order
+    }
+  }
+  __syncthreads();
+  if (t < ndig) hist[(size_t)t * gridDim.x + blockIdx.x] = cnt[t];
+  if (first_pass)
+    for (int r = blockIdx.x * kSortThreads + t; r < R; r += gridDim.x * kSortThreads) first[r] = last[r] = 0;
+}
+
+// exclusive scan over the blocks of one digit (one block per digit)
+__global__ __launch_bounds__(256) void sort_scan_kernel(int nblk, int* __restrict__ hist, int* __restrict__ total) {
+  __shared__ int sums[4];
+  const int t = threadIdx.x, lane = t % 64, w = t / 64;
+  int* h = hist + (size_t)blockIdx.x * nblk;
+  int carry = 0;
+  for (int b0 = 0; b0 < nblk; b0 += 256) {
+    const int v = b0 + t < nblk ? h[b0 + t] : 0;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 63) sums[w] = s;
+    __syncthreads();
+    int before = carry, all = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < w) before += sums[i];
+      all += sums[i];
+    }
+    if (b0 + t < nblk) h[b0 + t] = before + s - v;
+    carry += all;
+    __syncthreads();
+  }
+  if (t == 0) total[blockIdx.x] = carry;
+}
+
+// Stable scatter: a wave takes 64 neighbouring keys at a time, finds the
+// lanes with its digit by one ballot per bit, and counts on from its own
+// earlier keys; waves and blocks follow in order.
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(int N, int R, int shift, int bits, bool first_pass,
+                                                                    const int* __restrict__ keys,
+                                                                    const int* __restrict__ ord,
+                                                                    const int* __restrict__ hist,
+                                                                    const int* __restrict__ total,
+                                                                    int* __restrict__ keys_out,
+                                                                    int* __restrict__ ord_out) {
+  __shared__ int cnt[kSortWaves][256];
+  __shared__ int sums[kSortWaves];
+  const int t = threadIdx.x, lane = t % 64, w = t / 64, ndig = 1 << bits;
+#pragma unroll
+  for (int i = 0; i < kSortWaves; ++i) cnt[i][t] = 0;
+  __syncthreads();
+  const int base = blockIdx.x * kSortItems + w * (kSortItems / kSortWaves);
+  int key[kSortRounds], rank[kSortRounds];
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    const int n = base + i * 64 + lane;
+    const bool in = n < N;
+    key[i] = in ? (first_pass ? key_of(keys[n], R) : keys[n]) : 0;
+    const int d = (key[i] >> shift) & (ndig - 1);
+    unsigned long long peers = __ballot(in);
+    for (int b = 0; b < bits; ++b) {
+      const bool set = (d >> b) & 1;
+      const unsigned long long m = __ballot(in && set);
+      peers &= set ? m : ~m;
+    }
+    const int below = __popcll(peers & ((1ull << lane) - 1));
+    rank[i] = in ? cnt[w][d] + below : 0;
+    // every lane has read its count before the last peer adds the group
+    // (a wave's LDS accesses are served in order; the fences hold the compiler)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (in && (peers >> lane) == 1ull) cnt[w][d] = rank[i] + 1;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  __syncthreads();
+  {  // digit t: first position = digits before + blocks before + waves before
+    const int v = t < ndig ? total[t] : 0;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 63) sums[w] = s;
+    __syncthreads();
+    int run = s - v;
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i)
+      if (i < w) run += sums[i];
+    if (t < ndig) run += hist[(size_t)t * gridDim.x + blockIdx.x];
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) {
+      const int c = cnt[i][t];
+      cnt[i][t] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    const int n = base + i * 64 + lane;
+    if (n >= N) continue;
+    const int p = cnt[w][(key[i] >> shift) & (ndig - 1)] + rank[i];
+    keys_out[p] = key[i];
+    ord_out[p] = first_pass ? n : ord[n];
+  }
+}
+
+// ---------------------------------------------------------------- the sums --
+
+// One group of `group` lanes per (chunk, channel slice); lane i of the group
+// holds V channels.  part[chunk][2][C]: the sum of the run that begins at or
+// before the chunk's first token and does not end inside it alone (slot 0),
+// and of the run that begins inside and continues behind the chunk (slot 1).
+template <class T, int V>
+__global__ __launch_bounds__(256) void embed_sum_kernel(int N, int R, int C, int chunk, int chunks, int group,
+                                                        int slices, float scale, const int* __restrict__ key,
+                                                        const int* __restrict__ ord, const T* __restrict__ g,
+                                                        float* __restrict__ grad, float* __restrict__ part,
+                                                        int* __restrict__ first, int* __restrict__ last) {
+  const int per = 256 / group;
+  const long long item = (long long)blockIdx.x * per + threadIdx.x / group;
+  const int ch = int(item / slices), c = (int(item % slices) * group + threadIdx.x % group) * V;
+  if (ch >= chunks) return;
+  const bool live = c < C, lead = c == 0;
+  const int p0 = ch * chunk, p1 = min(N, p0 + chunk);
+  const int before = p0 > 0 ? key[p0 - 1] : -1, after = p1 < N ? key[p1] : -1;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  int cur = key[p0], begin = p0;
+  auto flush = [&](int end) {
+    // the run [begin, end) of row cur inside this chunk
+    const bool from_before = begin == p0 && before == cur, goes_on = end == p1 && after == cur;
+    if (lead) {
+      if (!from_before) first[cur] = begin;
+      if (!goes_on) last[cur] = end;
+    }
+    if (!live) return;
+    float* dst;
+    float f = 1.f;
+    if (!from_before && !goes_on) {
+      dst = grad + (size_t)cur * C;
+      f = scale;
+    } else {
+      dst = part + ((size_t)ch * 2 + (from_before || begin == p0 ? 0 : 1)) * C;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] *= f;
+    store_f32<float, V>(dst + c, acc);
+  };
+  constexpr int U = 8;   // rows in flight
+  for (int p = p0; p < p1; p += U) {
+    int k[U];
+    float x[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = min(p + u, p1 - 1);
+      k[u] = key[q];
+      if (live && k[u] < R) load_f32<T, V>(g + (size_t)ord[q] * C + c, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (p + u >= p1) break;
+      if (k[u] != cur) {
+        flush(p + u);
+        cur = k[u];
+        begin = p + u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+      }
+      if (cur >= R) return;   // padding is sorted last
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += x[u][i];
+    }
+  }
+  flush(p1);
+}
+
+// Rows whose run is cut by chunk edges, and rows without a token.  Each wave
+// takes a row; rows of more than kLong pieces are left to the whole block,
+// whose waves take pieces in turn and add up in wave order.
+constexpr int kLong = 16;
+template <int W, int V>
+__global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int chunk, float scale, int rows,
+                                                            const int* __restrict__ first,
+                                                            const int* __restrict__ last,
+                                                            const float* __restrict__ part, float* __restrict__ grad) {
+  __shared__ float sum[W][64 * V];
+  const int w = threadIdx.x / 64, lane = threadIdx.x % 64;
+  const int r0 = blockIdx.x * rows, r1 = min(R, r0 + rows);
+  // piece j of the run of chunks a..b: slot 1 of a unless the run begins there
+  auto slot = [&](int f, int ch) { return part + ((size_t)ch * 2 + (ch * chunk < f ? 1 : 0)) * C; };
+  for (int r = r0 + w; r < r1; r += W) {
+    const int f = first[r], l = last[r];
+    const int a = f / chunk, b = (l - 1) / chunk;
+    if (l > f && (a == b || b - a >= kLong)) continue;
+    for (int c = lane * V; c < C; c += 64 * V) {
+      float acc[V] = {};
+      for (int ch = a; l > f && ch <= b; ++ch) {
+        float x[V];
+        load_f32<float, V>(slot(f, ch) + c, x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += x[i];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] *= scale;
+      store_f32<float, V>(grad + (size_t)r * C + c, acc);
+    }
+  }
+  for (int r = r0; r < r1; ++r) {
+    const int f = first[r], l = last[r];
+    const int a = f / chunk, b = (l - 1) / chunk;
+    if (l <= f || b - a < kLong) continue;   // the same for the whole block
+    for (int c0 = 0; c0 < C; c0 += 64 * V) {
+      const int c = c0 + lane * V;
+      float acc[V] = {};
+      if (c < C) {
+#pragma unroll 4
+        for (int ch = a + w; ch <= b; ch += W) {
+          float x[V];
+          load_f32<float, V>(slot(f, ch) + c, x);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += x[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[w][lane * V + i] = acc[i];
+      __syncthreads();
+      if (w == 0 && c < C) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float t = 0.f;
+          for (int j = 0; j < W; ++j) t += sum[j][lane * V + i];
+          acc[i] = t * scale;
+        }
+        store_f32<float, V>(grad + (size_t)r * C + c, acc);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+int pow2_at_least(int n) {
+  int p = 1;
+  while (p < n) p <<= 1;
+  return p;
+}
+
+// channels per lane: 16 bytes of the element type where rows allow it
+int vec_of(int C, bool bf16, bool aligned) {
+  const int v = bf16 ? 8 : 4;
+  return aligned && C % v == 0 ? v : 1;
+}
+
+template <class T, int V>
+void fwd_t(int N, int R, int C, float scale, const void* table, const int* ids, void* out, hipStream_t st) {
+  const int x = std::min(64, pow2_at_least((C + V - 1) / V)), y = 256 / x;
+  hipLaunchKernelGGL((embed_fwd_kernel<T, V>), dim3((N + y - 1) / y), dim3(x, y), 0, st, N, R, C, scale,
+                     static_cast<const T*>(table), ids, static_cast<T*>(out));
+}
+
+template <class T, int V>
+void sum_t(const EmbedPlan& p, float scale, const int* key, const int* ord, const void* g, float* grad,
+           hipStream_t st) {
+  const int per = 256 / p.group;
+  const long long items = (long long)p.chunks * p.slices;
+  hipLaunchKernelGGL((embed_sum_kernel<T, V>), dim3((unsigned)((items + per - 1) / per)), dim3(256), 0, st, p.N, p.R,
+                     p.C, p.chunk, p.chunks, p.group, p.slices, scale, key, ord, static_cast<const T*>(g), grad, p.part,
+                     p.first, p.last);
+}
+
+template <int W, int V>
+void join_t(const EmbedPlan& p, float scale, float* grad, int rows, hipStream_t st) {
+  hipLaunchKernelGGL((embed_join_kernel<W, V>), dim3((p.R + rows - 1) / rows), dim3(W * 64), 0, st, p.R, p.C, p.chunk,
+                     scale, rows, p.first, p.last, p.part, grad);
+}
+
+}  // namespace
+
+EmbedPlan embed_plan(int N, int R, int C, bool bf16, bool aligned, void* ws) {
+  EmbedPlan p{};
+  p.N = N, p.R = R, p.C = C;
+  int bits = 1;
+  while ((1ll << bits) < (long long)R + 1) ++bits;   // keys 0..R
+  p.passes = (bits + 7) / 8;
+  p.bits = (bits + p.passes - 1) / p.passes;
+  p.sort_blocks = (N + kSortItems - 1) / kSortItems;
+  p.vec = vec_of(C, bf16, aligned);
+  const int pieces = (C + p.vec - 1) / p.vec;
+  p.group = std::min(64, pow2_at_least(pieces));
+  p.slices = (pieces + p.group - 1) / p.group;
+  // chunks of 32 tokens at least (the partial sums then stay below a
+  // sixteenth of what is read), longer once 16 waves per CU have one each
+  const long long groups = 256ll * 16 * (64 / p.group);
+  const long long want = (long long)N * p.slices / groups;
+  p.chunk = (int)std::clamp<long long>((want + 31) / 32 * 32, 32, 512);
+  p.chunks = (N + p.chunk - 1) / p.chunk;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += (n + 255) / 256 * 256;
+    return static_cast<char*>(ws) + o;
+  };
+  for (int i = 0; i < 2; ++i) {
+    p.key[i] = reinterpret_cast<int*>(take(sizeof(int) * (size_t)N));
+    p.ord[i] = reinterpret_cast<int*>(take(sizeof(int) * (size_t)N));
+  }
+  p.hist = reinterpret_cast<int*>(take(sizeof(int) * ((size_t)p.sort_blocks << p.bits)));
+  p.total = reinterpret_cast<int*>(take(sizeof(int) * 256));
+  p.first = reinterpret_cast<int*>(take(sizeof(int) * (size_t)R));
+  p.last = reinterpret_cast<int*>(take(sizeof(int) * (size_t)R));
+  p.part = reinterpret_cast<float*>(take(sizeof(float) * (size_t)p.chunks * 2 * C));
+  p.bytes = at;
+  return p;
+}
+
+void launch_embed_fwd(int N, int R, int C, bool is_bf16, bool aligned, float scale, const void* table, const int* ids,
+                      void* out, hipStream_t st) {
+  const int v = vec_of(C, is_bf16, aligned);
+  if (is_bf16)
+    v > 1 ? fwd_t<bf16, 8>(N, R, C, scale, table, ids, out, st) : fwd_t<bf16, 1>(N, R, C, scale, table, ids, out, st);
+  else
+    v > 1 ? fwd_t<float, 4>(N, R, C, scale, table, ids, out, st) : fwd_t<float, 1>(N, R, C, scale, table, ids, out, st);
+}
+
+void launch_embed_vjp(const EmbedPlan& p, bool is_bf16, float scale, const int* ids, const void* g, float* grad,
+                      hipStream_t st) {
+  const int ndig = 1 << p.bits;
+  const int* key = ids;
+  const int* ord = nullptr;
+  for (int s = 0; s < p.passes; ++s) {
+    int *ko = p.key[s & 1], *oo = p.ord[s & 1];
+    hipLaunchKernelGGL(sort_count_kernel, dim3(p.sort_blocks), dim3(kSortThreads), 0, st, p.N, p.R, s * p.bits, ndig,
+                       s == 0, key, p.hist, p.first, p.last);
+    hipLaunchKernelGGL(sort_scan_kernel, dim3(ndig), dim3(256), 0, st, p.sort_blocks, p.hist, p.total);
+    hipLaunchKernelGGL(sort_scatter_kernel, dim3(p.sort_blocks), dim3(kSortThreads), 0, st, p.N, p.R, s * p.bits,
+                       p.bits, s == 0, key, ord, p.hist, p.total, ko, oo);
+    key = ko;
+    ord = oo;
+  }
+  if (is_bf16)
+    p.vec > 1 ? sum_t<bf16, 8>(p, scale, key, ord, g, grad, st) : sum_t<bf16, 1>(p, scale, key, ord, g, grad, st);
+  else
+    p.vec > 1 ? sum_t<float, 4>(p, scale, key, ord, g, grad, st) : sum_t<float, 1>(p, scale, key, ord, g, grad, st);
+  // few rows: a block of 16 waves for each; many: four waves for several rows
+  const int rows = std::clamp(p.R / 4096, 1, 16);
+  if (rows == 1)
+    p.vec > 1 ? join_t<16, 4>(p, scale, grad, 1, st) : join_t<16, 1>(p, scale, grad, 1, st);
+  else
+    p.vec > 1 ? join_t<4, 4>(p, scale, grad, rows, st) : join_t<4, 1>(p, scale, grad, rows, st);
+}
+
+}  // namespace fc

@@ -20,6 +20,9 @@ FC_CONV_ALL_PARITIES = 1   # descriptor flag: every triangle-allowed path (odd J
 FC_CONV_SUM_PATHS = 2      # descriptor flag: outputs of the paths of each rank summed
 FC_CONV_MLP_MATERIALIZE = 4  # descriptor flag: radial-network calls store w [E][P][C] instead of fusing it
 FC_CONV_MLP_FUSE = 8         # descriptor flag: radial-network calls form w in the convolution's lanes
+FC_F32, FC_BF16 = 0, 1     # element types of the embedding, query/key norm and attention calls
+FC_ROPE_INTERLEAVED = 1    # descriptor flag: rotated pairs are neighbours (2t, 2t + 1)
+FC_ATTN_CAUSAL = 1         # descriptor flag: a query sees the prefix and the keys up to its own place
 
 
 class FlashCartError(RuntimeError):
@@ -50,6 +53,30 @@ class NormDesc(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class EmbedDesc(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class QkRopeDesc(ctypes.Structure):
+    _fields_ = [("n_nodes", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("n_freq", ctypes.c_int32), ("q_stride", ctypes.c_int32),
+                ("k_stride", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("n_query", ctypes.c_int32), ("n_key", ctypes.c_int32), ("n_segments", ctypes.c_int32),
+                ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("q_stride", ctypes.c_int32), ("k_stride", ctypes.c_int32), ("v_stride", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("cap", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
+class SegmentPtrs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -58,6 +85,10 @@ _PD = ctypes.POINTER(ConvDesc)
 _PL = ctypes.POINTER(LadderDesc)
 _PG = ctypes.POINTER(Graph)
 _PN = ctypes.POINTER(NormDesc)
+_PE = ctypes.POINTER(EmbedDesc)
+_PQ = ctypes.POINTER(QkRopeDesc)
+_PA = ctypes.POINTER(AttnDesc)
+_PS = ctypes.POINTER(SegmentPtrs)
 _PI = ctypes.POINTER(ctypes.c_int32)
 _PSZ = ctypes.POINTER(ctypes.c_size_t)
 
@@ -92,6 +123,16 @@ _SIGS = {
     "fc_rms_norm_fwd": (_I, [_PN, _P, _P, _P, _P, _P]),
     "fc_rms_norm_workspace_bytes": (_SZ, [_PN]),
     "fc_rms_norm_vjp": (_I, [_PN, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "fc_embed_fwd": (_I, [_PE, _P, _P, _P, _P]),
+    "fc_embed_workspace_bytes": (_SZ, [_PE]),
+    "fc_embed_vjp": (_I, [_PE, _P, _P, _P, _P, _SZ, _P]),
+    "fc_qk_norm_rope_fwd": (_I, [_PQ, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "fc_qk_norm_rope_workspace_bytes": (_SZ, [_PQ]),
+    "fc_qk_norm_rope_vjp": (_I, [_PQ, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "fc_segments_validate": (_I, [_I, _I, _PI]),
+    "fc_attention_workspace_bytes": (_SZ, [_PA, _I]),
+    "fc_attention_fwd": (_I, [_PA, _PS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "fc_attention_vjp": (_I, [_PA, _PS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "fc_message_block_weight_floats": (_SZ, [_PD, _PL]),
     "fc_message_block_workspace_bytes": (_SZ, [_PD, _PL]),
     "fc_message_block_energy_forces": (_I, [_PD, _PG, _P, _P, _P, _PL, _P, ctypes.c_float, ctypes.c_float, _P, _P,
@@ -438,3 +479,233 @@ def fc_message_block_energy_forces(conv: ConvDesc, graph: DeviceGraph, pos, shif
                                                 ctypes.c_float(conv_scale), ctypes.c_float(eps),
                                                 _ptr(energy, torch.float64), _f32(e_atom), _f32(forces),
                                                 _ptr(workspace), nbytes, _stream(stream)))
+
+
+# ------------------------------------------- embedding, queries/keys, attention --
+#
+# These calls check dtype, shape and device of every tensor against the
+# descriptor, and run on the tensors' device (its current stream by default).
+
+def embed_desc(n_tokens, n_rows, channels, scale=1.0, dtype=FC_F32) -> EmbedDesc:
+    return EmbedDesc(n_tokens, n_rows, channels, dtype, scale)
+
+
+def qk_rope_desc(n_nodes, heads_q, heads_k, head_dim, n_freq, eps, dtype=FC_F32, flags=0) -> QkRopeDesc:
+    """Row strides of q and k are taken from the tensors of each call."""
+    return QkRopeDesc(n_nodes, heads_q, heads_k, head_dim, n_freq, 0, 0, dtype, eps, flags)
+
+
+def attn_desc(n_query, n_key, n_segments, heads_q, heads_k, head_dim, scale, cap=0.0, dtype=FC_F32,
+              flags=0) -> AttnDesc:
+    """Row strides of q, k and v are taken from the tensors of each call."""
+    return AttnDesc(n_query, n_key, n_segments, heads_q, heads_k, head_dim, 0, 0, 0, dtype, scale, cap, flags)
+
+
+def _bad(msg: str):
+    return FlashCartError(FC_ERR_INVALID_ARGUMENT, msg)
+
+
+class _Args:
+    """Marshals the tensors of one call: all on one GPU, of the given dtype
+    and shape, contiguous but for the row stride where one is allowed."""
+
+    def __init__(self, dtype: int, stream, workspace=None):
+        import torch
+        self.torch = torch
+        self.elem = torch.bfloat16 if dtype == FC_BF16 else torch.float32
+        self.device = None
+        self.stream = stream
+        self.ws = self(workspace, torch.uint8, None, "workspace")
+        self.ws_bytes = 0 if workspace is None else workspace.numel()
+
+    def __call__(self, t, dtype, shape, name):
+        if t is None:
+            return None
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensor must live on the GPU")
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError(f"{name}: tensor on {t.device}, the others on {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise _bad(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensor must be contiguous")
+        return t.data_ptr()
+
+    def f32(self, t, shape, name):
+        return self(t, self.torch.float32, shape, name)
+
+    def i32(self, t, shape, name):
+        return self(t, self.torch.int32, shape, name)
+
+    def data(self, t, shape, name):
+        return self(t, self.elem, shape, name)
+
+    def rows(self, t, shape, name):
+        """(pointer, row stride in elements; 0 for packed rows)"""
+        if t is None or not isinstance(t, self.torch.Tensor) or t.is_contiguous():
+            return self(t, self.elem, shape, name), 0
+        if t.shape != shape:
+            raise _bad(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if (shape[2] > 1 and t.stride(2) != 1) or (shape[1] > 1 and t.stride(1) != shape[2]):
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        stride = t.stride(0)
+        if stride < shape[1] * shape[2]:
+            raise _bad(f"{name}: rows overlap (stride {stride})")
+        self(t[:1], self.elem, None, name)   # device and dtype
+        return t.data_ptr(), stride
+
+    def call(self, f, *args):
+        torch = self.torch
+        if self.device is None:
+            return _check(f(*args, self._stream_of(None)))
+        if self.device.index == torch.cuda.current_device():
+            return _check(f(*args, self._stream_of(self.device)))
+        with torch.cuda.device(self.device):
+            _check(f(*args, self._stream_of(self.device)))
+
+    def _stream_of(self, device):
+        s = self.stream
+        if s is None:
+            s = self.torch.cuda.current_stream(device)
+        return getattr(s, "cuda_stream", s)
+
+
+def fc_embed_fwd(d: EmbedDesc, table, ids, out, stream=None):
+    a = _Args(d.dtype, stream)
+    a.call(lib().fc_embed_fwd, d, a.data(table, (d.n_rows, d.channels), "table"), a.i32(ids, (d.n_tokens,), "ids"),
+           a.data(out, (d.n_tokens, d.channels), "out"))
+
+
+def fc_embed_workspace_bytes(d: EmbedDesc) -> int:
+    return lib().fc_embed_workspace_bytes(d)
+
+
+def fc_embed_vjp(d: EmbedDesc, ids, g_out, table_grad, workspace, stream=None):
+    a = _Args(d.dtype, stream, workspace)
+    a.call(lib().fc_embed_vjp, d, a.i32(ids, (d.n_tokens,), "ids"),
+           a.data(g_out, (d.n_tokens, d.channels), "g_out"),
+           a.f32(table_grad, (d.n_rows, d.channels), "table_grad"), a.ws, a.ws_bytes)
+
+
+def _qk_inputs(a: _Args, d: QkRopeDesc, q, k, gamma_q, gamma_k, pos, freq):
+    n, dim = d.n_nodes, d.head_dim
+    pq, sq = a.rows(q, (n, d.heads_q, dim), "q")
+    pk, sk = a.rows(k, (n, d.heads_k, dim), "k")
+    if sq or sk:
+        d = QkRopeDesc.from_buffer_copy(d)
+        d.q_stride, d.k_stride = sq, sk
+    return (d, pq, pk, a.f32(gamma_q, (dim,), "gamma_q"), a.f32(gamma_k, (dim,), "gamma_k"),
+            a.f32(pos, (n, 3), "pos"), a.f32(freq, (d.n_freq, 3), "freq"))
+
+
+def fc_qk_norm_rope_fwd(d: QkRopeDesc, q, k, gamma_q, gamma_k, pos, freq, q_out, k_out, stream=None):
+    a = _Args(d.dtype, stream)
+    n, dim = d.n_nodes, d.head_dim
+    a.call(lib().fc_qk_norm_rope_fwd, *_qk_inputs(a, d, q, k, gamma_q, gamma_k, pos, freq),
+           a.data(q_out, (n, d.heads_q, dim), "q_out"), a.data(k_out, (n, d.heads_k, dim), "k_out"))
+
+
+def fc_qk_norm_rope_workspace_bytes(d: QkRopeDesc) -> int:
+    return lib().fc_qk_norm_rope_workspace_bytes(d)
+
+
+def fc_qk_norm_rope_vjp(d: QkRopeDesc, q, k, gamma_q, gamma_k, pos, freq, g_q, g_k, q_grad, k_grad, gamma_q_grad,
+                        gamma_k_grad, pos_grad, workspace, stream=None):
+    a = _Args(d.dtype, stream, workspace)
+    n, dim = d.n_nodes, d.head_dim
+    sq, sk = (n, d.heads_q, dim), (n, d.heads_k, dim)
+    a.call(lib().fc_qk_norm_rope_vjp, *_qk_inputs(a, d, q, k, gamma_q, gamma_k, pos, freq),
+           a.data(g_q, sq, "g_q"), a.data(g_k, sk, "g_k"), a.data(q_grad, sq, "q_grad"), a.data(k_grad, sk, "k_grad"),
+           a.f32(gamma_q_grad, (dim,), "gamma_q_grad"), a.f32(gamma_k_grad, (dim,), "gamma_k_grad"),
+           a.f32(pos_grad, (n, 3), "pos_grad"), a.ws, a.ws_bytes)
+
+
+def fc_segments_validate(n_segments: int, n_rows: int, offsets) -> None:
+    """Host array (numpy int32)."""
+    import numpy as np
+    o = np.ascontiguousarray(offsets, dtype=np.int32)
+    if o.shape != (n_segments + 1,):
+        raise _bad(f"{o.size} offsets for {n_segments} segments")
+    _check(lib().fc_segments_validate(n_segments, n_rows, o.ctypes.data_as(_PI)))
+
+
+class Segments:
+    """Segment offsets (structures of a batch, documents) on the GPU.
+
+    ``offsets_q`` [S+1] gives the first query row of each segment,
+    ``offsets_k`` the first key row (None: the same rows), ``prefix`` [S] the
+    number of leading keys that every query sees under ``FC_ATTN_CAUSAL``.
+    The host copies are checked before they are uploaded.
+    """
+
+    def __init__(self, offsets_q, offsets_k=None, prefix=None, device="cuda"):
+        import numpy as np
+        import torch
+        host = lambda a: np.asarray(torch.as_tensor(a).cpu().numpy(), dtype=np.int64)
+        q = host(offsets_q)
+        k = q if offsets_k is None else host(offsets_k)
+        if q.ndim != 1 or q.size < 2 or k.shape != q.shape:
+            raise _bad("offsets need one entry per segment and the end, the same number for queries and keys")
+        self.n_segments = int(q.size) - 1
+        self.n_query, self.n_key = int(q[-1]), int(k[-1])
+        for o in (q, k):
+            if o.min() < 0 or o.max() > 2 ** 31 - 1:
+                raise _bad("offsets out of range")
+            fc_segments_validate(self.n_segments, int(o[-1]), o)
+        up = lambda a: torch.as_tensor(a.astype(np.int32), device=device)
+        self.q, self.k = up(q), None if offsets_k is None else up(k)
+        self.prefix = None
+        if prefix is not None:
+            p = host(prefix)
+            if p.shape != (self.n_segments,) or (p < 0).any() or (p > np.diff(k)).any():
+                raise _bad("prefix needs one length per segment, within its keys")
+            self.prefix = up(p)
+        ptr = lambda t: None if t is None else t.data_ptr()
+        self.struct = SegmentPtrs(ptr(self.q), ptr(self.k), ptr(self.prefix))
+
+
+def _attn_inputs(a: _Args, d: AttnDesc, seg, q, k, v, slope, pos_q, pos_k):
+    if seg is not None:
+        if seg.n_segments != d.n_segments:
+            raise _bad(f"{seg.n_segments} segments, the descriptor has {d.n_segments}")
+        if seg.n_query > d.n_query or seg.n_key > d.n_key:
+            raise _bad(f"segments end at rows {seg.n_query}, {seg.n_key}, beyond the descriptor's {d.n_query}, {d.n_key}")
+        a.i32(seg.q, None, "segments")
+    kv = (d.n_key, d.heads_k, d.head_dim)
+    pq, sq = a.rows(q, (d.n_query, d.heads_q, d.head_dim), "q")
+    pk, sk = a.rows(k, kv, "k")
+    pv, sv = a.rows(v, kv, "v")
+    if sq or sk or sv:
+        d = AttnDesc.from_buffer_copy(d)
+        d.q_stride, d.k_stride, d.v_stride = sq, sk, sv
+    return (d, None if seg is None else seg.struct, pq, pk, pv, a.f32(slope, (d.heads_q,), "slope"),
+            a.f32(pos_q, (d.n_query, 3), "pos_q"), a.f32(pos_k, (d.n_key, 3), "pos_k"))
+
+
+def fc_attention_workspace_bytes(d: AttnDesc, op: int) -> int:
+    return lib().fc_attention_workspace_bytes(d, op)
+
+
+def fc_attention_fwd(d: AttnDesc, seg, q, k, v, slope, pos_q, pos_k, out, lse, workspace, stream=None):
+    """``seg`` is a ``Segments`` or None (one segment of all rows)."""
+    a = _Args(d.dtype, stream, workspace)
+    a.call(lib().fc_attention_fwd, *_attn_inputs(a, d, seg, q, k, v, slope, pos_q, pos_k),
+           a.data(out, (d.n_query, d.heads_q, d.head_dim), "out"), a.f32(lse, (d.n_query, d.heads_q), "lse"), a.ws,
+           a.ws_bytes)
+
+
+def fc_attention_vjp(d: AttnDesc, seg, q, k, v, slope, pos_q, pos_k, out, lse, g_out, q_grad, k_grad, v_grad,
+                     slope_grad, pos_q_grad, pos_k_grad, workspace, stream=None):
+    a = _Args(d.dtype, stream, workspace)
+    qs, ks = (d.n_query, d.heads_q, d.head_dim), (d.n_key, d.heads_k, d.head_dim)
+    a.call(lib().fc_attention_vjp, *_attn_inputs(a, d, seg, q, k, v, slope, pos_q, pos_k), a.data(out, qs, "out"),
+           a.f32(lse, (d.n_query, d.heads_q), "lse"), a.data(g_out, qs, "g_out"), a.data(q_grad, qs, "q_grad"),
+           a.data(k_grad, ks, "k_grad"), a.data(v_grad, ks, "v_grad"), a.f32(slope_grad, (d.heads_q,), "slope_grad"),
+           a.f32(pos_q_grad, (d.n_query, 3), "pos_q_grad"), a.f32(pos_k_grad, (d.n_key, 3), "pos_k_grad"), a.ws,
+           a.ws_bytes)

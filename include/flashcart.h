@@ -10,11 +10,16 @@
  *     radial weights to the positions (forces);
  *   - its VJP-of-VJP for position cotangents, App. C Eq. C2;
  *   - the node-local correlation ladder, §5 Eq. 2 (full) and App. E
- *     "Path-reduced products", and its VJP.
+ *     "Path-reduced products", and its VJP;
+ * and, beside the pages' method, the operators of networks that let the atoms
+ * of a structure attend to each other: the scaled lookup of species (token)
+ * embeddings, the norm of queries and keys with a rotation by position, and
+ * attention with a distance bias, each with its VJP.
  *
  * Conventions shared by every call
  * --------------------------------
- * Precision: fp32 storage and arithmetic.
+ * Precision: fp32 storage and arithmetic.  The embedding, query/key norm and
+ *   attention calls also take bfloat16 arrays (fc_dtype) and compute in fp32.
  * Memory: every array argument is a DEVICE pointer into caller-owned memory.
  *   The library allocates nothing inside any call and keeps no pointer after
  *   return; scratch comes from a caller workspace sized by the matching
@@ -471,6 +476,164 @@ fc_status fc_rms_norm_vjp(const fc_norm_desc* d, const float* x, const float* ga
                           const float* inv_scale, const float* g_y, float* x_grad,
                           float* gamma_grad, void* workspace, size_t workspace_bytes,
                           hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Element type of the arrays that a descriptor with `dtype` names: fp32 or
+ * bfloat16.  Sums, norms, softmax statistics and angles are held in fp32 or
+ * more; each output is rounded once.  fp16 is not offered: score gradients
+ * leave its range.
+ * ---------------------------------------------------------------------- */
+typedef int32_t fc_dtype;
+#define FC_F32 0
+#define FC_BF16 1
+
+/* ------------------------------------------------------------------------
+ * Scaled embedding lookup: h0 of a message block (fc_message_block_energy_
+ * forces) from the species of its atoms, or rows of any token table.
+ *   out[n][c] = scale * table[ids[n]][c]
+ * table [n_rows][channels] and out [n_tokens][channels] have the element type
+ * `dtype`; ids int32 [n_tokens].  An id outside [0, n_rows) is padding: its
+ * output row is zero and it adds nothing to the gradient.  n_tokens >= 0,
+ * n_rows >= 1, channels >= 1, scale finite.  16-byte pieces are used where
+ * channels and pointers allow them; other sizes work element by element.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t n_tokens, n_rows, channels;
+  fc_dtype dtype;
+  float scale;
+} fc_embed_desc;
+
+fc_status fc_embed_fwd(const fc_embed_desc* d, const void* table, const int32_t* ids, void* out,
+                       hipStream_t stream);
+
+/* VJP of L = <g_out, out>: table_grad (fp32 [n_rows][channels] whatever
+ * `dtype`), the sum over the tokens of each row in a fixed order (tokens
+ * sorted by row), zero for rows without a token.  g_out [n_tokens][channels]
+ * of type `dtype`.  Needs fc_embed_workspace_bytes(d) bytes (256-byte
+ * aligned). */
+size_t fc_embed_workspace_bytes(const fc_embed_desc* d);
+fc_status fc_embed_vjp(const fc_embed_desc* d, const int32_t* ids, const void* g_out, float* table_grad,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * RMS norm of every query and key head with the rotation by position, in one
+ * pass.  For a head row x of head_dim elements of node n at position p_n:
+ *   y = gamma x / sqrt(mean(x^2) + eps),   theta_t = <freq_t, p_n>,
+ *   (o1, o2) = (y1 cos theta_t - y2 sin theta_t, y1 sin theta_t + y2 cos theta_t)
+ * for the n_freq rotated pairs t; the other elements pass as y.  Pair t is
+ * (t, t + n_freq), or (2t, 2t + 1) with FC_ROPE_INTERLEAVED.
+ * freq [n_freq][3] are wave vectors (radians per unit of pos), so that scores
+ * depend on differences of positions; token positions are pos = (i, 0, 0).
+ * Angles are formed in fp64.  q [n_nodes][heads_q][head_dim] and
+ * k [n_nodes][heads_k][head_dim] of type `dtype`, rows q_stride / k_stride
+ * elements apart (0: packed), so that both may be parts of one projection's
+ * output; q_out, k_out and every gradient are packed.  gamma_q, gamma_k: fp32
+ * [head_dim], NULL for ones; pos, freq: fp32, both NULL for no rotation.
+ * heads_k = 0 (k, k_out NULL) treats the queries alone (gamma_k_grad is then
+ * zero).  n_nodes >= 0,
+ * heads_q >= 1, head_dim even and <= 128, 0 <= n_freq <= head_dim / 2, eps > 0.
+ * ---------------------------------------------------------------------- */
+#define FC_ROPE_INTERLEAVED 1u
+
+typedef struct {
+  int32_t n_nodes, heads_q, heads_k, head_dim, n_freq;
+  int32_t q_stride, k_stride;
+  fc_dtype dtype;
+  float eps;
+  uint32_t flags;
+} fc_qk_rope_desc;
+
+fc_status fc_qk_norm_rope_fwd(const fc_qk_rope_desc* d, const void* q, const void* k,
+                              const float* gamma_q, const float* gamma_k, const float* pos,
+                              const float* freq, void* q_out, void* k_out, hipStream_t stream);
+
+/* VJP of L = <g_q, q_out> + <g_k, k_out> at the forward's inputs: q_grad,
+ * k_grad (type `dtype`), gamma_q_grad, gamma_k_grad (fp32 [head_dim], summed
+ * over nodes and heads in a fixed order) and pos_grad (fp32 [n_nodes][3]),
+ * each when non-NULL (at least one).  freq is a constant.  A gamma gradient
+ * needs fc_qk_norm_rope_workspace_bytes(d) bytes. */
+size_t fc_qk_norm_rope_workspace_bytes(const fc_qk_rope_desc* d);
+fc_status fc_qk_norm_rope_vjp(const fc_qk_rope_desc* d, const void* q, const void* k,
+                              const float* gamma_q, const float* gamma_k, const float* pos,
+                              const float* freq, const void* g_q, const void* g_k, void* q_grad,
+                              void* k_grad, float* gamma_q_grad, float* gamma_k_grad, float* pos_grad,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention among the rows of each segment (the atoms of one structure of a
+ * batch; a document).  For query row i and key row j of one segment, query
+ * head h and its key head h / (heads_q / heads_k):
+ *   u = scale <q_i, k_j>,  t = cap tanh(u / cap) (t = u when cap = 0),
+ *   s = t - slope_h |pos_q_i - pos_k_j|,
+ *   out_i = sum_j softmax_j(s) v_j,  lse_i = log sum_j exp(s)
+ * over the keys that i sees: every key of its segment, or with
+ * FC_ATTN_CAUSAL those with j < prefix or j <= i + (Lk - Lq), where i, j
+ * count from the segment's first row and Lq, Lk are its lengths (the last
+ * query sees every key).  A row that sees no key has out = 0, lse = -inf and
+ * adds nothing to any gradient.
+ * q [n_query][heads_q][head_dim], k and v [n_key][heads_k][head_dim] of type
+ * `dtype`, rows *_stride elements apart (0: packed); out and every gradient
+ * are packed; lse fp32 [n_query][heads_q].  slope fp32 [heads_q], pos_q fp32
+ * [n_query][3], pos_k fp32 [n_key][3]; slope NULL: no bias.  pos_k NULL: the
+ * keys are the queries' atoms (n_key = n_query, segments->k NULL).
+ * Distances are between the given points (no periodic images); their
+ * gradient is 0 at distance 0.
+ * Requirements: n_query, n_key >= 0, n_segments >= 1, heads_k >= 1,
+ * heads_q <= 256 a multiple of heads_k, head_dim a multiple of 8 and <= 128,
+ * scale > 0, cap >= 0; q, k, v, out, g_out and their gradients 16-byte
+ * aligned with strides of whole 16-byte pieces.
+ * Values inside a segment must be finite, also those a causal mask hides;
+ * rows behind the last segment may hold anything: they are not read, and
+ * their outputs and gradients are left as they were.
+ * In bfloat16 the probabilities and the score gradients are rounded to
+ * bfloat16 as operands of the matrix cores; statistics and the position and
+ * slope gradients stay in fp32.
+ * Few queries over many keys (and the reverse) are split over the long axis;
+ * the workspace holds the parts.  Calls that may run at the same time (two
+ * streams, two graphs) need a workspace each.
+ * ---------------------------------------------------------------------- */
+#define FC_ATTN_CAUSAL 1u
+
+typedef struct {
+  int32_t n_query, n_key, n_segments;
+  int32_t heads_q, heads_k, head_dim;
+  int32_t q_stride, k_stride, v_stride;
+  fc_dtype dtype;
+  float scale, cap;
+  uint32_t flags;
+} fc_attn_desc;
+
+typedef struct {
+  const int32_t* q;      /* [S+1] first query row of each segment; NULL: one segment  */
+  const int32_t* k;      /* [S+1] first key row of each segment; NULL: the same as q  */
+  const int32_t* prefix; /* [S] keys that every query of the segment sees, or NULL    */
+} fc_segments;
+
+/* Host check of segment offsets (HOST array): offsets[0] = 0, none smaller
+ * than the one before, the last at most n_rows.  The device calls clamp
+ * offsets to their arrays, so bad ones give wrong rows but no access outside. */
+fc_status fc_segments_validate(int32_t n_segments, int32_t n_rows, const int32_t* offsets);
+
+/* Workspace of one call.  op 0: forward, 1: VJP; 256-byte aligned. */
+size_t fc_attention_workspace_bytes(const fc_attn_desc* d, int32_t op);
+
+fc_status fc_attention_fwd(const fc_attn_desc* d, const fc_segments* seg, const void* q, const void* k,
+                           const void* v, const float* slope, const float* pos_q, const float* pos_k,
+                           void* out, float* lse, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* VJP of L = <g_out, out> at the forward's inputs, out and lse: q_grad,
+ * k_grad, v_grad (type `dtype`), slope_grad (fp32 [heads_q]), pos_q_grad and
+ * pos_k_grad (fp32), each when non-NULL (at least one).  With pos_k NULL the
+ * position gradient comes whole in pos_q_grad and pos_k_grad must be NULL.
+ * Gradients of shared key heads are summed over their query heads.  Every
+ * sum has a fixed order: results are bitwise reproducible. */
+fc_status fc_attention_vjp(const fc_attn_desc* d, const fc_segments* seg, const void* q, const void* k,
+                           const void* v, const float* slope, const float* pos_q, const float* pos_k,
+                           const void* out, const float* lse, const void* g_out, void* q_grad,
+                           void* k_grad, void* v_grad, float* slope_grad, float* pos_q_grad,
+                           float* pos_k_grad, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
 
 #ifdef __cplusplus
 }
