@@ -27,6 +27,11 @@ FLAGS = [
     "-I" + CSRC, "-I" + os.path.join(ROOT, "include"),
     "-Wno-unused-command-line-argument",
 ]
+# flags of single units.  The attention kernels work on every matrix result
+# with vector instructions, so results stay in vector registers (through
+# accumulation registers each element costs a move).
+UNIT_FLAGS = {f"fc_attn_{t}_{d}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+              for t in ("f32", "bf16") for d in (16, 32, 64, 128)}
 
 
 def sources():
@@ -42,7 +47,7 @@ def _obj(src: str) -> str:
 
 def _compile(src: str) -> str:
     obj = _obj(src)
-    cmd = [HIPCC, *FLAGS, "-c", src, "-o", obj]
+    cmd = [HIPCC, *FLAGS, *UNIT_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj]
     t = time.time()
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -36,6 +36,7 @@ namespace {
 // kernels count in 32 bits stays below 2^31
 constexpr int kMaxRows = 1 << 30;
 constexpr int kMaxHeads = 1024;
+constexpr int kMaxStride = 1 << 22;
 
 thread_local std::string g_msg;
 
@@ -383,6 +384,8 @@ fc_status check_attn(const fc_attn_desc* d) {
       return fail(FC_ERR_INVALID_ARGUMENT,
                   "attention: %c_stride %d is shorter than a row or not a whole number of 16-byte pieces", "qkv"[i],
                   strides[i]);
+  for (int32_t s : strides)   // the offsets inside a row tile are 32 bits
+    if (s > kMaxStride) return fail(FC_ERR_UNSUPPORTED, "attention: strides above %d are not supported", kMaxStride);
   return check_dtype("attention", d->dtype);
 }
 

@@ -43,17 +43,28 @@ struct AttnPart {
   float* o;       // fwd: [splits][nq hq][D], normalised per split; VJP: partial gradients
   float* o2;      // VJP over keys: partial value gradients [splits][nk hk][D]
   float* lse;     // fwd: [splits][nq hq]
-  float* delta;   // VJP: [dsplits][nq hq], written by the delta pass
-  int dsplits;
+  float* delta;   // VJP: [dsplits][nq hq]
+  int dsplits;    // 1 unless the delta pass is split
+  bool exact;     // delta comes from the delta pass, else the query pass forms <g, out>
   float* row;     // VJP: [splits][nq hq][4] position and slope gradients of a query row, or null
   float* col;     // VJP: [splits][nk hk][4] position gradients of a key row, or null
 };
 
 enum AttnPass { kAttnFwd, kAttnDelta, kAttnQuery, kAttnKey };
+enum AttnMode { kOne, kCols, kRows };   // how the waves of a block share its work
 struct AttnLaunch {
   AttnPass pass;
-  int waves;      // waves per block (1 or 4), 32 columns each
+  AttnMode mode;
+  int hb;         // key heads per wave, 1 or (forward with a bias) 2
 };
+
+// Whether the forward may hold two key heads per wave (they share the
+// distances): their columns, accumulators and row tiles have to fit, and fp32
+// rows have three parts.  In the VJP one head per wave was as fast or faster
+// at every size (more waves fit).
+constexpr bool attn_two_heads(bool bf16, int DP) { return DP <= (bf16 ? 64 : 32); }
+// Row tiles too large for a wave alone: kCols is the only mode.
+constexpr bool attn_cols_only(bool bf16, int DP) { return !bf16 && DP > 64; }
 
 // One function per element type and padded head dimension (own units).
 template <class T, int DP>

@@ -63,27 +63,6 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(int n, int width, int S, 
   store_f32<T, 4>(out + at, x);
 }
 
-// delta[row] = <out, g> of a query row and head; eight lanes per row
-template <class T>
-__global__ __launch_bounds__(256) void attn_dot_kernel(AttnArgs a, float* __restrict__ delta) {
-  const size_t rows = (size_t)a.nq * a.hq, row = ((size_t)blockIdx.x * 256 + threadIdx.x) / 8;
-  float s = 0.f;
-  if (row < rows) {
-    const T* o = static_cast<const T*>(a.out) + row * a.D;
-    const T* g = static_cast<const T*>(a.g) + row * a.D;
-    for (int d = (threadIdx.x % 8) * 4; d < a.D; d += 32) {
-      float x[4], y[4];
-      load_f32<T, 4>(o + d, x);
-      load_f32<T, 4>(g + d, y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s = fmaf(x[i], y[i], s);
-    }
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) s += __shfl_xor(s, o);
-  if (row < rows && threadIdx.x % 8 == 0) delta[row] = s;
-}
-
 // position gradient of a row: its heads and splits in order; `self` adds the
 // part it has as a key
 __global__ __launch_bounds__(256) void attn_pos_kernel(int n, int S, const int* seg, int h0, int s0,
@@ -127,22 +106,34 @@ __global__ __launch_bounds__(256) void attn_slope_kernel(int n, int H, int S, co
 // ------------------------------------------------------------------- plans --
 
 struct PassPlan {
-  int waves, splits;
+  AttnMode mode;
+  int hb, splits;
 };
 
-// `cols` columns and `rows` walked rows in all, over S segments; `heads`
-// key heads.
-//  * Four waves share a row tile; where a segment's columns fill at most one
-//    and a half waves, a block is one wave.
-//  * The walk is split until the chip has two blocks (of four waves) per CU,
-//    in parts of 128 rows at least.
-PassPlan plan_pass(int64_t cols, int64_t rows, int S, int heads) {
+// `cols` columns and `rows` walked rows in all, over S segments; hk key heads.
+//  * kCols (four waves with a row tile in common) loads least.  It is taken
+//    where segments fill its 128 columns; long walks are split over blocks in
+//    parts of 1024 rows at least, while the chip has fewer than four blocks
+//    per CU.
+//  * Few columns over a long walk (single queries): four waves share the walk
+//    (kRows), and blocks in parts of 512 rows, up to two blocks per CU.
+//  * Few columns and rows (molecules): waves go alone (kOne).
+PassPlan plan_pass(const AttnArgs& a, bool is_bf16, AttnPass pass, int64_t cols, int64_t rows) {
   PassPlan p;
-  const int64_t mean = (cols + S - 1) / S;
-  p.waves = mean <= 48 ? 1 : 4;
-  const int64_t tiles = std::max<int64_t>(1, (mean + 32 * p.waves - 1) / (32 * p.waves)) * S * heads;
-  const int64_t want = 512 * 4 / p.waves / tiles, most = rows / S / 128;
-  p.splits = (int)std::clamp<int64_t>(std::min(want, most), 1, 64);
+  const int64_t mean = (cols + a.S - 1) / a.S, walk = rows / a.S;
+  auto splits = [&](int64_t blocks, int64_t want, int64_t part) {
+    return (int)std::clamp<int64_t>(std::min(want / std::max<int64_t>(1, blocks), walk / part), 1, 64);
+  };
+  p.hb = pass == kAttnFwd && a.slope && attn_two_heads(is_bf16, a.D) && a.hk % 2 == 0 && mean >= 32 ? 2 : 1;
+  const int64_t units = (int64_t)a.S * (a.hk / p.hb);
+  if (mean >= 96 || attn_cols_only(is_bf16, a.D)) {
+    const int64_t blocks = (mean + 127) / 128 * units;
+    p.mode = kCols, p.splits = mean >= 96 ? splits(blocks, 960, 1024) : splits(blocks, 512, 128);
+  } else if (walk >= 256) {
+    p.mode = kRows, p.splits = splits((mean + 31) / 32 * units, 512, 512);
+  } else {
+    p.mode = kOne, p.splits = 1;
+  }
   return p;
 }
 
@@ -158,8 +149,9 @@ struct Plan {
 Plan make_plan(const AttnArgs& a, bool is_bf16, int op, void* ws) {
   Plan p{};
   const int64_t cq = (int64_t)a.nq * a.G;
-  p.fwd = p.query = plan_pass(cq, a.nk, a.S, a.hk);
-  p.key = plan_pass(a.nk, cq, a.S, a.hk);
+  p.fwd = plan_pass(a, is_bf16, kAttnFwd, cq, a.nk);
+  p.query = plan_pass(a, is_bf16, kAttnQuery, cq, a.nk);
+  p.key = plan_pass(a, is_bf16, kAttnKey, a.nk, cq);
   // Position and slope gradients are fp32 outputs; with delta from a
   // bfloat16 out they would carry its rounding.
   p.exact_delta = is_bf16 && a.slope && (a.g_slope || a.g_pos_q || a.g_pos_k);
@@ -178,6 +170,7 @@ Plan make_plan(const AttnArgs& a, bool is_bf16, int op, void* ws) {
     }
   } else {
     AttnPart c{};
+    c.exact = p.exact_delta;
     c.dsplits = p.exact_delta ? p.query.splits : 1;
     c.delta = take(c.dsplits * rq);
     if (a.slope) {
@@ -243,7 +236,7 @@ size_t attn_workspace_bytes(const AttnArgs& a, bool is_bf16, int op) {
 void launch_attn_fwd(const AttnArgs& a, bool is_bf16, void* ws, hipStream_t st) {
   if (a.nq == 0) return;
   const Plan p = make_plan(a, is_bf16, 0, ws);
-  launch_pass(is_bf16, {kAttnFwd, p.fwd.waves}, a, p.pf, st);
+  launch_pass(is_bf16, {kAttnFwd, p.fwd.mode, p.fwd.hb}, a, p.pf, st);
   if (p.fwd.splits == 1) return;
   const dim3 g(blocks_of((size_t)a.nq * a.hq * (a.D / 4)));
   if (is_bf16)
@@ -254,24 +247,14 @@ void launch_attn_fwd(const AttnArgs& a, bool is_bf16, void* ws, hipStream_t st) 
 
 void launch_attn_vjp(const AttnArgs& a, bool is_bf16, void* ws, hipStream_t st) {
   const Plan p = make_plan(a, is_bf16, 1, ws);
-  if (a.nq > 0) {
-    if (p.exact_delta) {
-      launch_pass(is_bf16, {kAttnDelta, p.query.waves}, a, p.pd, st);
-    } else {
-      const dim3 g(blocks_of((size_t)a.nq * a.hq * 8));
-      if (is_bf16)
-        hipLaunchKernelGGL(attn_dot_kernel<bf16>, g, dim3(256), 0, st, a, p.pd.delta);
-      else
-        hipLaunchKernelGGL(attn_dot_kernel<float>, g, dim3(256), 0, st, a, p.pd.delta);
-    }
-    if (a.gq || a.g_slope || a.g_pos_q) {
-      launch_pass(is_bf16, {kAttnQuery, p.query.waves}, a, p.pq, st);
-      if (p.query.splits > 1)
-        sum_splits(is_bf16, a.nq, a.hq * a.D, a.S, a.seg_q, p.query.splits, p.pq.o, a.gq, st);
-    }
+  if (a.nq > 0) {   // also for the key pass alone: it leaves delta
+    if (p.exact_delta) launch_pass(is_bf16, {kAttnDelta, p.query.mode, p.query.hb}, a, p.pd, st);
+    launch_pass(is_bf16, {kAttnQuery, p.query.mode, p.query.hb}, a, p.pq, st);
+    if (p.query.splits > 1)
+      sum_splits(is_bf16, a.nq, a.hq * a.D, a.S, a.seg_q, p.query.splits, p.pq.o, a.gq, st);
   }
   if (a.nk > 0 && (a.gk || a.gv || a.g_pos_k || (a.g_pos_q && a.self_pos))) {
-    launch_pass(is_bf16, {kAttnKey, p.key.waves}, a, p.pk, st);
+    launch_pass(is_bf16, {kAttnKey, p.key.mode, p.key.hb}, a, p.pk, st);
     if (p.key.splits > 1) {
       sum_splits(is_bf16, a.nk, a.hk * a.D, a.S, a.seg_k, p.key.splits, p.pk.o, a.gk, st);
       sum_splits(is_bf16, a.nk, a.hk * a.D, a.S, a.seg_k, p.key.splits, p.pk.o2, a.gv, st);

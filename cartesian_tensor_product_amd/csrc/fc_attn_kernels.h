@@ -20,7 +20,14 @@
 // lane: maxima and sums over rows stay in the lane (plus one exchange between
 // the wave's halves), and the same registers are the right-hand operand of
 // the second product, whose left-hand side is the row tile read transposed
-// (ds_read_b64_tr_b16 for bfloat16, plain reads for fp32).
+// (ds_read_b64_tr_b16).
+//
+// fp32 rows are split into three bfloat16 parts, x = h + m + l without a
+// remainder, and a product of two of them into the six partial products down
+// to 2^-16 of the largest (the three left out are below 2^-25).  The fp32
+// matrix instruction runs on the vector units: per 32 x 32 x 2 it takes 74
+// cycles during which no vector instruction issues, 592 for a depth of 16; six
+// bfloat16 ones take 222 and vector work goes on meanwhile.
 //
 // No atomics: each output has one writer, and the VJP is two passes, which
 // repeats the scores (seven products instead of five) but keeps results
@@ -30,6 +37,7 @@
 #include <hip/hip_runtime.h>
 
 #include "fc_attn.h"
+#include "fc_common.h"
 #include "fc_types.h"
 
 namespace fc {
@@ -45,138 +53,264 @@ inline constexpr float kLog2e = 1.44269504088896340736f;
 inline constexpr float kLn2 = 0.69314718055994530942f;
 inline constexpr float kInf = __builtin_huge_valf();
 
-// 16 bytes of a row: the unit of every load, and one step of a product
+// 16 bytes of a row in memory: the unit of every load.  In LDS and in the
+// columns' registers there are bfloat16 parts, one or three.
 template <class T>
-struct Elem;
-template <>
-struct Elem<float> {
-  static constexpr int kChunk = 4;
-  using Frag = f32x4;
-};
-template <>
-struct Elem<bf16> {
-  static constexpr int kChunk = 8;
-  using Frag = bf16x8;
-};
+constexpr int kPieceOf = 16 / (int)sizeof(T);
+template <class T>
+constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
 
-// acc[row][col] += A[row][.] B[col][.] over two chunks (one per half wave)
-__device__ __forceinline__ f32x16 mma(f32x4 a, f32x4 b, f32x16 c) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
-  return c;
-}
 __device__ __forceinline__ f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+// acc += the small products of the parts of a and b.  They have a sum of
+// their own where it can be had (the matrix unit drops low bits of a term far
+// below its accumulator, towards minus infinity: a bias in long sums).
+__device__ __forceinline__ f32x16 mma_low(const bf16x8 (&a)[3], const bf16x8 (&b)[3], f32x16 c) {
+  c = mma(a[1], b[1], c);
+  c = mma(a[0], b[2], c);
+  c = mma(a[2], b[0], c);
+  c = mma(a[0], b[1], c);
+  return mma(a[1], b[0], c);
+}
+
+// x as bfloat16 parts, each rounded to nearest (one: the only rounding)
+template <int NP, int N, class V>
+__device__ __forceinline__ void split(const float (&x)[N], V (&p)[NP]) {
+  float r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = x[i];
+#pragma unroll
+  for (int k = 0; k < NP; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      p[k][i] = static_cast<bf16>(r[i]);
+      if (k + 1 < NP) r[i] -= static_cast<float>(p[k][i]);
+    }
 }
 
 // Row of register r of the 32x32 result, for the wave's half h.
 __device__ __forceinline__ constexpr int acc_row(int r, int h) { return (r / 4) * 8 + h * 4 + r % 4; }
 
-template <class T, int DP>
+// A tile of rows in LDS holds HB neighbouring heads of DP elements (padded
+// head dimension) per row.  The row length in LDS is an odd multiple of 16
+// bytes, so that 16 rows' chunks at one place spread over all banks; rows of
+// 256 bytes get 48 more rather than 16, so that also the four rows of a
+// transposing read meet at most in pairs.
+template <class T, int DP, int HB>
 struct Tile {
-  static constexpr int CH = Elem<T>::kChunk;
-  using Frag = typename Elem<T>::Frag;
-  static constexpr int STEPS = DP / (2 * CH);          // products over d
+  static constexpr int NP = kParts<T>, CH = kPieceOf<T>;
+  static constexpr int STEPS = DP / 16;                // products over d
   static constexpr int DB = (DP + 31) / 32;            // 32-wide blocks of d
-  static constexpr int LD = DB * 32 + CH;              // LDS row: 16 bytes of padding spread the banks
-  static constexpr int CPR = DP / CH;                  // chunks of a row
-  static_assert(DP % (2 * CH) == 0);
+  static constexpr int W = HB * DP;
+  static constexpr int LD = W + (DP < 32 ? 32 - DP : 0) + (W == 128 ? 24 : 8);
+  static constexpr int CPR = W / CH;                   // pieces of a row
+  static constexpr int PART = 32 * LD;                 // one part of 32 rows
+  struct Cols {
+    bf16x8 f[STEPS][NP];
+  };
 
-  // columns of a wave: lane -> its column's chunk 2 s + h
-  static __device__ __forceinline__ void load_cols(const T* row, bool live, int D, int h, Frag (&f)[STEPS]) {
+  // columns of a wave: lane -> its column's elements 16 s + 8 h ...
+  static __device__ __forceinline__ void load_cols(const T* row, bool live, int D, int h, Cols& c) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      const int d = (2 * s + h) * CH;
-      Frag z = {};
-      f[s] = live && d < D ? *reinterpret_cast<const Frag*>(row + d) : z;
+      const int d = 16 * s + 8 * h;
+      const bool in = live && d < D;
+      if constexpr (NP == 1) {
+        const bf16x8 z = {};
+        c.f[s][0] = in ? *reinterpret_cast<const bf16x8*>(row + d) : z;
+      } else {
+        const f32x4 z = {};
+        const f32x4 lo = in ? *reinterpret_cast<const f32x4*>(row + d) : z;
+        const f32x4 hi = in ? *reinterpret_cast<const f32x4*>(row + d + 4) : z;
+        const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        split(x, c.f[s]);
+      }
     }
   }
 
   // acc[row][col] = sum_d rows[row][d] cols[col][d] for 32 rows in LDS
-  static __device__ __forceinline__ f32x16 dot(const T* rows, const Frag (&cols)[STEPS], int lane) {
-    f32x16 c = {};
-    const T* p = rows + (lane % 32) * LD + (lane / 32) * CH;
+  static __device__ __forceinline__ f32x16 dot(const bf16* rows, const Cols& cols, int lane) {
+    f32x16 c = {}, low = {};
+    const bf16* p = rows + (lane % 32) * LD + (lane / 32) * 8;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) c = mma(*reinterpret_cast<const Frag*>(p + 2 * s * CH), cols[s], c);
+    for (int s = 0; s < STEPS; ++s) {
+      bf16x8 a[NP];
+#pragma unroll
+      for (int k = 0; k < NP; ++k) a[k] = *reinterpret_cast<const bf16x8*>(p + k * PART + 16 * s);
+      if constexpr (NP == 3) low = mma_low(a, cols.f[s], low);
+      c = mma(a[0], cols.f[s][0], c);
+    }
+    if constexpr (NP == 3) c += low;
     return c;
   }
 
-  // out[d][col] += sum_row rows[row][d] w[row][col] for 32 rows in LDS
-  static __device__ __forceinline__ void outer(const T* rows, const f32x16& w, f32x16 (&out)[DB], int lane) {
-    if constexpr (sizeof(T) == 4) {
-      const T* p = rows + (lane / 32) * 4 * LD + lane % 32;
+  // out[d][col] += sum_row rows[row][d] w[row][col] for 32 rows in LDS; the
+  // weights are split as the rows are (bfloat16: rounded)
+  static __device__ __forceinline__ void outer(const bf16* rows, const f32x16& w, f32x16 (&out)[DB], int lane) {
+    // 16 lanes read four rows x 16 columns and get a column each
+    const bf16* p = rows + ((lane / 32) * 4 + (lane % 16) / 4) * LD + ((lane / 16) % 2) * 16 + (lane % 4) * 4;
+    typedef __attribute__((address_space(3))) i16x4* lds_ptr;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const T* pr = p + acc_row(r, 0) * LD;
+    for (int s = 0; s < 2; ++s) {
+      float x[8];
 #pragma unroll
-        for (int b = 0; b < DB; ++b)
-          out[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(pr[b * 32], w[r], out[b], 0, 0, 0);
-      }
-    } else {
-      // 16 lanes read four rows x 16 columns and get a column each
-      const T* p = rows + ((lane / 32) * 4 + (lane % 16) / 4) * LD + ((lane / 16) % 2) * 16 + (lane % 4) * 4;
-      typedef __attribute__((address_space(3))) i16x4* lds_ptr;
+      for (int i = 0; i < 8; ++i) x[i] = w[8 * s + i];
+      bf16x8 wb[NP];
+      split(x, wb);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        bf16x8 wb;   // rounded to bfloat16 as the matrix instruction takes it
+      for (int b = 0; b < DB; ++b) {
+        bf16x8 a[NP];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wb[i] = static_cast<bf16>(w[8 * s + i]);
-#pragma unroll
-        for (int b = 0; b < DB; ++b) {
-          const T* pb = p + s * 16 * LD + b * 32;
+        for (int k = 0; k < NP; ++k) {
+          const bf16* pb = p + k * PART + s * 16 * LD + b * 32;
           const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(pb)));
           const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(pb + 8 * LD)));
-          out[b] = mma(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), wb, out[b]);
+          a[k] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
+        if constexpr (NP == 3) out[b] = mma_low(a, wb, out[b]);
+        out[b] = mma(a[0], wb[0], out[b]);
       }
     }
   }
 };
 
-// A tile of ROWS rows on its way from memory to LDS: loaded into registers
-// while the tile before is worked on, then stored.
-template <class T, int DP, int ROWS, int THREADS>
+// Buffer offsets are 32 bits from a base that moves with the tile; an offset
+// of kNowhere lies behind every buffer and reads zeros.
+constexpr uint32_t kNowhere = 0x7ffffff0u, kReach = 0x7fffff00u;
+
+// bytes from row `row` to the end of `n` rows of `stride` bytes (the last one
+// `last` bytes long), as the reach of a buffer
+__device__ __forceinline__ uint32_t reach(int row, int n, int64_t stride, int last) {
+  return row < n ? (uint32_t)min((int64_t)kReach, (n - 1 - row) * stride + last) : 0u;
+}
+
+// A tile on its way from memory to LDS: loaded into registers while the tile
+// before is worked on, then stored.  Loads are buffer loads, without branches:
+// what lies behind the segment's last row reads as zero.
+template <class T, int DP, int HB, int ROWS, int TH>
 struct Stage {
-  using TL = Tile<T, DP>;
-  static constexpr int N = (ROWS * TL::CPR + THREADS - 1) / THREADS;
+  using TL = Tile<T, DP, HB>;
+  static constexpr int N = (ROWS * TL::CPR + TH - 1) / TH;
+  static constexpr int STEP = TH / TL::CPR;   // rows from one turn to the next
+  static_assert(TH % TL::CPR == 0 && (N == 1 || ROWS * TL::CPR % TH == 0) && ROWS % 32 == 0);
   f32x4 r[N];
 
-  // row(i) gives the address of tile row i, null for a row of zeros
-  template <class F>
-  __device__ __forceinline__ void load(int D, F&& row) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = i * THREADS + threadIdx.x;
-      const int rr = e / TL::CPR, d = (e % TL::CPR) * TL::CH;
-      f32x4 z = {};
-      r[i] = z;
-      if ((ROWS * TL::CPR % THREADS == 0 || rr < ROWS) && d < D) {
-        const T* p = row(rr);
-        if (p) r[i] = *reinterpret_cast<const f32x4*>(p + d);
-      }
-    }
+  // The thread's place t: tile rows t / CPR + n STEP, and bytes inside a row.
+  static __device__ __forceinline__ uint32_t place(int t, int D, int head_stride) {
+    const int c = t % TL::CPR, d = c % (DP / TL::CH) * TL::CH;
+    return t / TL::CPR < ROWS && d < D ? (uint32_t)(c / (DP / TL::CH) * head_stride + d) * sizeof(T) : kNowhere;
   }
-  __device__ __forceinline__ void store(T* lds) const {
+  // row(r): byte offset of tile row r from the buffer's base (below 2^31, so
+  // that kNowhere stays out of reach)
+  template <class F>
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buf, int t, uint32_t place, F&& row) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = i * THREADS + threadIdx.x;
-      const int rr = e / TL::CPR, d = (e % TL::CPR) * TL::CH;
-      if (ROWS * TL::CPR % THREADS == 0 || rr < ROWS) *reinterpret_cast<f32x4*>(lds + rr * TL::LD + d) = r[i];
+    for (int n = 0; n < N; ++n)
+      r[n] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, place + row(t / TL::CPR + n * STEP), 0, 0));
+  }
+  // off: place and row of each turn
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buf, const uint32_t (&off)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      r[n] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off[n], 0, 0));
+  }
+  // 32 rows after 32 rows, each with its parts
+  __device__ __forceinline__ void store(int t, bf16* lds) const {
+    if (ROWS * TL::CPR < TH && t >= ROWS * TL::CPR) return;
+    const int col = t % TL::CPR * TL::CH;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int row = t / TL::CPR + n * STEP;
+      bf16* p = lds + row / 32 * (TL::NP * TL::PART) + row % 32 * TL::LD + col;
+      if constexpr (TL::NP == 1) {
+        *reinterpret_cast<f32x4*>(p) = r[n];
+      } else {
+        const float x[4] = {r[n][0], r[n][1], r[n][2], r[n][3]};
+        bf16x4 s[TL::NP];
+        split(x, s);
+#pragma unroll
+        for (int k = 0; k < TL::NP; ++k) *reinterpret_cast<bf16x4*>(p + k * TL::PART) = s[k];
+      }
     }
   }
 };
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
-
-// tanh from one exponential; its error is that of 1 - tanh, a few 2^-24
-__device__ __forceinline__ float tanh_fast(float x) {
-  return 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (2.f * kLog2e)));
+// Keeps what depends on x inside its branch (few tiles have an edge).
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
+
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+__device__ __forceinline__ f32x4 four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+
+// tanh.  fp32 rows: within a few 2^-24 of its value also near 0, where one
+// exponential alone would lose digits.  bfloat16 rows: the exponential alone,
+// a few 2^-24 in absolute terms.
+template <class T>
+__device__ __forceinline__ float tanh_of(float x) {
+  const float e = __builtin_amdgcn_exp2f(x * (2.f * kLog2e));
+  const float far = fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + e), 1.f);
+  if constexpr (sizeof(T) == 2) return far;
+  const float z = x * x;   // Taylor series; |x| < 0.4 leaves z^7 below 2^-24
+  float p = fmaf(z, 21844.f / 6081075.f, -1382.f / 155925.f);
+  p = fmaf(z, p, 62.f / 2835.f);
+  p = fmaf(z, p, -17.f / 315.f);
+  p = fmaf(z, p, 2.f / 15.f);
+  p = fmaf(z, p, -1.f / 3.f);
+  return z < 0.16f ? fmaf(x * z, p, x) : far;
+}
+
+// 1 / r of a squared distance.  Squares carry 1e-35, so that at r = 0 this is
+// a large finite value, which meets differences that are 0 there.
+__device__ __forceinline__ float inv_dist(float r2) { return __builtin_amdgcn_rsqf(r2); }
+// r from it; fp32 rows get a Newton step, since slope r may be tens
+template <class T>
+__device__ __forceinline__ float dist_of(float r2, float inv) {
+  const float r = r2 * inv;
+  return sizeof(T) == 2 ? r : fmaf(0.5f * inv, fmaf(-r, r, r2), r);
+}
+
+// (a + b) log 2, rounded once: the products' and the sum's rests are kept, since
+// an error of lse scales a whole row's probabilities in the VJP
+__device__ __forceinline__ float ln_of(float a, float b) {
+  constexpr float kLn2Rest = -1.90465429995776804525e-9f;   // log 2 - kLn2
+  const float s = a + b, rest = fabsf(a) > fabsf(b) ? (a - s) + b : (b - s) + a;
+  const float p = s * kLn2;
+  return p + (fmaf(s, kLn2, -p) + fmaf(s, kLn2Rest, rest * kLn2));
+}
+
+// lse for the VJP: probabilities are exp2(score - ref) factor with a whole
+// number ref, so that the rest of lse / log 2 is not rounded with it.  A row
+// that sees no key (lse = -inf) gets ref = inf: its probabilities vanish.
+struct Norm {
+  float ref, factor;
+  __device__ __forceinline__ explicit Norm(float lse) {
+    constexpr float kLog2eRest = 1.92596299112661746887e-8f;   // 1 / log 2 - kLog2e
+    const float x = lse * kLog2e, rest = fmaf(lse, kLog2e, -x) + lse * kLog2eRest;
+    const bool some = fabsf(lse) < kInf;
+    ref = some ? rintf(x) : kInf;
+    factor = some ? __builtin_amdgcn_exp2f((ref - x) - rest) : 1.f;
+  }
+};
+
+// Differences and distances from a column's point to four rows' points.
+struct Points {
+  f32x4 dx, dy, dz;
+  __device__ __forceinline__ Points(float px, float py, float pz, const float* x, const float* y, const float* z)
+      : dx(px - four(x)), dy(py - four(y)), dz(pz - four(z)) {}
+  __device__ __forceinline__ float square(int e) const { return fmaf(dx[e], dx[e], fmaf(dy[e], dy[e], fmaf(dz[e], dz[e], 1e-35f))); }
+  // g += f (p - row)
+  __device__ __forceinline__ void add(int e, float f, float (&g)[3]) const {
+    g[0] = fmaf(f, dx[e], g[0]), g[1] = fmaf(f, dy[e], g[1]), g[2] = fmaf(f, dz[e], g[2]);
+  }
+};
 
 // ------------------------------------------------- which work a block has --
 
 struct Work {
-  int seg, tile, head, split;   // segment, column tile in it, key head
+  int tile, head, split;   // column tile in its segment, first key head
   int q0, lq, k0, lk, pre;
   bool any;
 };
@@ -184,16 +318,16 @@ struct Work {
 // Tiles of `cols` columns: segment s starts at tile off[s] mul / cols + s,
 // which leaves every segment room for its last, partial tile without a scan
 // over the segments before it (at most one tile per segment stays empty).
-__device__ __forceinline__ int64_t tile_start(const int* off, int s, int mul, int cols) {
-  return (off ? (int64_t)off[s] * mul / cols : 0) + s;
+__device__ __forceinline__ int64_t tile_start(int off, int s, int mul, int cols) {
+  return (int64_t)off * mul / cols + s;
 }
 
 // The column axis is queries (mul = G) or keys (mul = 1).  All lanes of a
-// wave search together, 64 segments per step.
+// wave search together.
 template <bool KEYS>
-__device__ __forceinline__ Work find_work(const AttnArgs& a, int cols, int tiles, int splits) {
+__device__ __forceinline__ Work find_work(const AttnArgs& a, int cols, int hb, int tiles, int splits) {
   Work w{};
-  const int units = a.hk * splits;
+  const int heads = a.hk / hb, units = heads * splits;
   int unit, t;
   const int b = blockIdx.x;
   // Blocks go to the eight dies in turn.  A die takes whole (key head, split)
@@ -210,29 +344,45 @@ __device__ __forceinline__ Work find_work(const AttnArgs& a, int cols, int tiles
     t = b / units;
   }
   if (t >= tiles || unit >= units) return w;
-  t = tiles - 1 - t;   // causal: the long columns come first
-  w.head = unit % a.hk;
-  w.split = unit / a.hk;
-  const int* off = KEYS ? a.seg_k : a.seg_q;
-  const int mul = KEYS ? 1 : a.G;
-  int lo = 0, hi = a.S;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 63) / 64;
-    const int s = lo + (int)(threadIdx.x % 64) * step;
-    const bool le = s < hi && tile_start(off, s, mul, cols) <= t;
-    const int n = max(1, __popcll(__ballot(le)));   // offsets out of order stay in range
-    lo += (n - 1) * step;
-    hi = min(hi, lo + step);
-  }
-  w.seg = __builtin_amdgcn_readfirstlane(lo);
-  w.tile = t - (int)tile_start(off, w.seg, mul, cols);
-  // offsets are clamped to the arrays: bad ones give wrong rows, not bad reads
+  if (!KEYS) t = tiles - 1 - t;   // causal: the long columns (late queries, early keys) come first
+  w.head = unit % heads * hb;
+  w.split = unit / heads;
   auto clamp = [](int x, int l, int h) { return min(max(x, l), h); };
-  w.q0 = a.seg_q ? clamp(a.seg_q[w.seg], 0, a.nq) : 0;
-  w.lq = (a.seg_q ? clamp(a.seg_q[w.seg + 1], w.q0, a.nq) : a.nq) - w.q0;
-  w.k0 = a.seg_k ? clamp(a.seg_k[w.seg], 0, a.nk) : 0;
-  w.lk = (a.seg_k ? clamp(a.seg_k[w.seg + 1], w.k0, a.nk) : a.nk) - w.k0;
-  w.pre = a.causal && a.prefix ? clamp(a.prefix[w.seg], 0, w.lk) : 0;
+  const int* off = KEYS ? a.seg_k : a.seg_q;
+  const int n = KEYS ? a.nk : a.nq, mul = KEYS ? 1 : a.G, lane = threadIdx.x % 64;
+  int seg = 0, c0 = 0, c1 = n;
+  if (off) {
+    int lo = 0, hi = a.S;
+    while (hi - lo > 63) {   // 64 candidates per step
+      const int step = (hi - lo + 63) / 64, s = lo + lane * step;
+      const bool le = s < hi && tile_start(off[min(s, hi)], s, mul, cols) <= t;
+      lo += (max(1, __popcll(__ballot(le))) - 1) * step;
+      hi = min(hi, lo + step);
+    }
+    const int s = min(lo + lane, hi), o = off[s];
+    const bool le = lo + lane < hi && tile_start(o, s, mul, cols) <= t;
+    const int at = max(1, __popcll(__ballot(le))) - 1;   // offsets out of order stay in range
+    seg = __builtin_amdgcn_readfirstlane(lo + at);
+    // offsets are clamped to the arrays: bad ones give wrong rows, not bad reads
+    const int o0 = __builtin_amdgcn_readlane(o, at), o1 = __builtin_amdgcn_readlane(o, at + 1);
+    w.tile = t - (int)tile_start(o0, seg, mul, cols);
+    c0 = clamp(o0, 0, n);
+    c1 = clamp(o1, c0, n);
+  } else {
+    w.tile = t;
+  }
+  const int* other = KEYS ? a.seg_q : a.seg_k;
+  const int no = KEYS ? a.nq : a.nk;
+  int r0 = c0, r1 = c1;
+  if (other != off) {
+    r0 = other ? clamp(other[seg], 0, no) : 0;
+    r1 = other ? clamp(other[seg + 1], r0, no) : no;
+  } else if (!off) {
+    r1 = no;
+  }
+  w.q0 = KEYS ? r0 : c0, w.lq = KEYS ? r1 - r0 : c1 - c0;
+  w.k0 = KEYS ? c0 : r0, w.lk = KEYS ? c1 - c0 : r1 - r0;
+  w.pre = a.causal && a.prefix ? clamp(a.prefix[seg], 0, w.lk) : 0;
   w.any = w.tile >= 0 && (int64_t)w.tile * cols < (int64_t)(KEYS ? w.lk : w.lq) * mul;
   return w;
 }
@@ -249,508 +399,770 @@ __device__ __forceinline__ void split_range(int n, int unit, int splits, int spl
   hi = min(n, lo + per);
 }
 
-// Key positions of a tile, one array per coordinate.
-template <int ROWS>
-struct PosTile {
-  float x[ROWS], y[ROWS], z[ROWS];
+// How the waves of a block share its work.
+//  kOne: one wave, 32 columns.  kCols: four waves with 32 columns each, every
+//  row tile loaded once for all.  kRows: four waves with the same 32 columns,
+//  each with its own row tiles (every fourth), joined through LDS at the end.
+template <int MODE>
+struct Waves {
+  static constexpr int NW = MODE == kOne ? 1 : 4;
+  static constexpr int TH = NW * 64;
+  static constexpr int COLS = MODE == kCols ? 128 : 32;
+  static constexpr int REGIONS = MODE == kRows ? 4 : 1;       // row tiles in LDS
+  static constexpr int STAGE = MODE == kCols ? 256 : 64;      // threads that fill one
+  static constexpr int STRIDE = MODE == kRows ? 4 : 1;        // tiles from one to the next of a wave
+  static __device__ __forceinline__ int stage_thread() { return MODE == kCols ? threadIdx.x : threadIdx.x % 64; }
+  static __device__ __forceinline__ int region() { return MODE == kRows ? threadIdx.x / 64 : 0; }
+  // between the writes and the reads of a tile
+  static __device__ __forceinline__ void sync() {
+    if constexpr (MODE == kCols)
+      __syncthreads();
+    else   // a wave's LDS accesses are served in order; this holds the compiler
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
 };
 
-__device__ __forceinline__ f32x4 four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+// ------------------------------------------------- results of a wave's columns --
+
+// out(hb, d, x): four elements from d of head hb, for the lane's column
+template <int HB, int DB, class F>
+__device__ __forceinline__ void each_piece(const f32x16 (&o)[HB][DB], int h, int D, F&& out) {
+#pragma unroll
+  for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const int d = b * 32 + r4 * 8 + h * 4;
+        const float x[4] = {o[hb][b][r4 * 4], o[hb][b][r4 * 4 + 1], o[hb][b][r4 * 4 + 2], o[hb][b][r4 * 4 + 3]};
+        if (d < D) out(hb, d, x);
+      }
+}
+
+// kRows: adds the four waves' results, in wave order.  slices: LDS of the row
+// tiles, free by now, `slice` floats per wave.  out(col, hb, d, x) is called
+// once per piece, neighbouring threads with neighbouring d.
+template <int HB, int DB, class F>
+__device__ __forceinline__ void join_waves(float* slices, int slice, const f32x16 (&o)[HB][DB], int D, F&& out) {
+  const int lane = threadIdx.x % 64, h = lane / 32, W = HB * D + 4;
+  float* mine = slices + threadIdx.x / 64 * slice + lane % 32 * W;
+  __syncthreads();
+  each_piece(o, h, D, [&](int hb, int d, const float* x) { store_f32<float, 4>(mine + hb * D + d, x); });
+  __syncthreads();
+  const int per = HB * D / 4;
+  for (int e = threadIdx.x; e < 32 * per; e += 256) {
+    const int col = e / per, c = (e - col * per) * 4;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float y[4];
+      load_f32<float, 4>(slices + w * slice + col * W + c, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] += y[i];
+    }
+    out(col, c / D, c % D, x);
+  }
+}
+
+// sum over the four waves of a value per (n, column), in wave order; buf
+// holds 4 x N x 32 floats
+template <int N>
+__device__ __forceinline__ void join_values(float* buf, float (&v)[N]) {
+  const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
+  __syncthreads();
+  if (lane < 32)
+#pragma unroll
+    for (int i = 0; i < N; ++i) buf[(w * N + i) * 32 + lane] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t += buf[(k * N + i) * 32 + lane % 32];
+    v[i] = t;
+  }
+}
+
+// Waves per SIMD that a kernel's registers allow: columns and accumulators of
+// all heads, `live` 32x32 results at a time, the tile on its way, and what
+// goes into addresses, scalars and reads ahead from LDS, out of 512.
+template <class T, int DP, int HB, int MODE, bool BIAS>
+constexpr int waves_per_simd(int frags, int accs, int live, int rows) {
+  using TL = Tile<T, DP, HB>;
+  const int regs = frags * HB * TL::STEPS * TL::NP * 4 + accs * HB * TL::DB * 16 + live * 16 +
+                   2 * 4 * ((rows * TL::CPR + Waves<MODE>::STAGE - 1) / Waves<MODE>::STAGE) + (BIAS ? 100 : 60);
+  return regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+}
 
 // ---------------------------------------------------------------- forward --
 
-template <class T, int DP, int NW, int NS, bool BIAS, bool CAP>
-__global__ __launch_bounds__(NW * 64) void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
-  using TL = Tile<T, DP>;
-  constexpr int ROWS = 32 * NS, COLS = 32 * NW, TH = NW * 64;
-  __shared__ __align__(16) T lk[ROWS * TL::LD];
-  __shared__ __align__(16) T lv[ROWS * TL::LD];
-  __shared__ __align__(16) PosTile<BIAS ? ROWS : 4> lp;
-  const Work w = find_work<false>(a, COLS, tiles, part.splits);
+// The softmax in one pass, in units of log 2.  Scores are formed relative to
+// a reference m per column, which follows the running maximum: it is raised
+// (and what was added so far is scaled down) at the first tile and when a
+// score exceeds it by 2^kSlack, so most tiles need neither a subtraction nor a
+// scaling.  The keys a column sees are the first ones, so a column that sees
+// none in a wave's first tile sees none at all there.
+constexpr float kSlack = 8.f;
+
+template <class T, int HB, int MODE>
+constexpr int fwd_rows() {
+  return sizeof(T) == 2 && HB == 1 && MODE == kCols ? 64 : 32;
+}
+
+template <class T, int DP, int HB, int MODE, bool BIAS, bool CAP>
+__global__ __launch_bounds__(Waves<MODE>::TH, (waves_per_simd<T, DP, HB, MODE, BIAS>(1, 1, fwd_rows<T, HB, MODE>() / 32 * (1 + BIAS), fwd_rows<T, HB, MODE>())))
+void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
+  using TL = Tile<T, DP, HB>;
+  using WV = Waves<MODE>;
+  constexpr int ROWS = fwd_rows<T, HB, MODE>(), NS = ROWS / 32;
+  constexpr int AREA = ROWS * TL::LD * TL::NP;   // LDS of one row tile
+  __shared__ __align__(16) bf16 lds[WV::REGIONS * 2 * AREA];
+  __shared__ __align__(16) float lpos[BIAS ? WV::REGIONS * 3 * ROWS : 4];
+  const Work w = find_work<false>(a, WV::COLS, HB, tiles, part.splits);
   if (!w.any) return;   // the whole block
-  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32;
-  const int col = w.tile * COLS + wv * 32 + lane % 32;
-  const int i = col / a.G, head = w.head * a.G + col % a.G;
+  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32, st = WV::stage_thread();
+  const int col = w.tile * WV::COLS + (MODE == kCols ? wv * 32 : 0) + lane % 32;
+  const int i = col / a.G, head = w.head * a.G + col % a.G;   // + hb G for the other heads
   const bool live = i < w.lq;
   const size_t qrow = w.q0 + i;
-  typename TL::Frag qf[TL::STEPS];
-  TL::load_cols(static_cast<const T*>(a.q) + (live ? qrow * a.qs + (size_t)head * a.D : 0), live, a.D, h, qf);
-  float px = 0.f, py = 0.f, pz = 0.f, slope = 0.f;
-  if (BIAS && live) {
-    px = a.pos_q[3 * qrow], py = a.pos_q[3 * qrow + 1], pz = a.pos_q[3 * qrow + 2];
-    slope = a.slope[head] * kLog2e;
-  }
+  bf16 *lk = lds + WV::region() * 2 * AREA, *lv = lk + AREA;
+  float* lp = lpos + (BIAS ? WV::region() * 3 * ROWS : 0);
+
   const int vis = live ? visible(a, w, i) : 0;
   // the last column of the block sees the most
-  const int iend = min(w.lq, (w.tile * COLS + COLS - 1) / a.G + 1);
+  const int iend = min(w.lq, (w.tile * WV::COLS + WV::COLS - 1) / a.G + 1);
   int kb, ke;
   split_range(visible(a, w, iend - 1), ROWS, part.splits, w.split, kb, ke);
-  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+  if (MODE == kRows) kb += wv * ROWS;
 
-  f32x16 o[TL::DB];
-#pragma unroll
-  for (int b = 0; b < TL::DB; ++b) o[b] = f32x16{};
-  float m = -kInf, l = 0.f;
-
-  Stage<T, DP, ROWS, TH> sk, sv;
-  float sp[3] = {0.f, 0.f, 0.f};
+  Stage<T, DP, HB, ROWS, WV::STAGE> sk, sv;
+  const uint32_t place = sk.place(st, a.D, a.D);
+  float sp[3];
   const T* kbase = static_cast<const T*>(a.k) + (size_t)w.k0 * a.ks + (size_t)w.head * a.D;
   const T* vbase = static_cast<const T*>(a.v) + (size_t)w.k0 * a.vs + (size_t)w.head * a.D;
+  const uint32_t kst = (uint32_t)a.ks * sizeof(T), vst = (uint32_t)a.vs * sizeof(T);
+  const int row_bytes = HB * a.D * (int)sizeof(T);
   auto fetch = [&](int j0) {
-    sk.load(a.D, [&](int r) { return j0 + r < ke ? kbase + (size_t)(j0 + r) * a.ks : nullptr; });
-    sv.load(a.D, [&](int r) { return j0 + r < ke ? vbase + (size_t)(j0 + r) * a.vs : nullptr; });
-    if (BIAS && threadIdx.x < ROWS)
+    sk.load(make_rsrc(kbase + (size_t)j0 * a.ks, reach(j0, w.lk, kst, row_bytes)), st, place,
+            [&](int r) { return r * kst; });
+    sv.load(make_rsrc(vbase + (size_t)j0 * a.vs, reach(j0, w.lk, vst, row_bytes)), st, place,
+            [&](int r) { return r * vst; });
+    if constexpr (BIAS) {
+      const auto buf = make_rsrc(a.pos_k + 3 * (size_t)(w.k0 + j0), reach(j0, w.lk, 12, 12));
 #pragma unroll
       for (int c = 0; c < 3; ++c)
-        sp[c] = j0 + (int)threadIdx.x < ke ? a.pos_k[3 * (size_t)(w.k0 + j0 + threadIdx.x) + c] : 0.f;
+        sp[c] = buf_load(buf, st < ROWS ? st * 12 + c * 4 : kNowhere, 0);
+    }
   };
   if (kb < ke) fetch(kb);
-  for (int j0 = kb; j0 < ke; j0 += ROWS) {
-    __syncthreads();   // the tile before has been read
-    sk.store(lk);
-    sv.store(lv);
-    if (BIAS && threadIdx.x < ROWS) lp.x[threadIdx.x] = sp[0], lp.y[threadIdx.x] = sp[1], lp.z[threadIdx.x] = sp[2];
-    __syncthreads();
-    if (j0 + ROWS < ke) fetch(j0 + ROWS);
 
-    f32x16 s[NS];
+  typename TL::Cols qf[HB];
+  float slope[HB], m[HB], l[HB];
+  f32x16 o[HB][TL::DB];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) s[n] = TL::dot(lk + n * 32 * TL::LD, qf, lane);
-    // scores in units of log 2
+  for (int hb = 0; hb < HB; ++hb) {
+    const int hq = head + hb * a.G;
+    TL::load_cols(static_cast<const T*>(a.q) + (live ? qrow * a.qs + (size_t)hq * a.D : 0), live, a.D, h, qf[hb]);
+    slope[hb] = BIAS && live ? a.slope[hq] * kLog2e : 0.f;
+    m[hb] = l[hb] = 0.f;
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        f32x4 kx, ky, kz;
-        if constexpr (BIAS) {
-          const int j = n * 32 + r4 * 8 + h * 4;
-          kx = four(lp.x + j), ky = four(lp.y + j), kz = four(lp.z + j);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[n][r4 * 4 + e] * c1;
-          if constexpr (CAP) x = c2 * tanh_fast(x);
-          if constexpr (BIAS) {
-            const float dx = px - kx[e], dy = py - ky[e], dz = pz - kz[e];
-            x = fmaf(-slope, __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz))), x);
-          }
-          s[n][r4 * 4 + e] = x;
-        }
-      }
-    if (__any(j0 + ROWS > vis))
+    for (int b = 0; b < TL::DB; ++b) o[hb][b] = f32x16{};
+  }
+  float px = 0.f, py = 0.f, pz = 0.f;
+  if (BIAS && live) px = a.pos_q[3 * qrow], py = a.pos_q[3 * qrow + 1], pz = a.pos_q[3 * qrow + 2];
+  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+
+  bool first = true;
+  auto tile = [&](bool edge, int j0) {
+    f32x16 dist[NS];
+    if constexpr (BIAS)
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (j0 + n * 32 + acc_row(r, h) >= vis) s[n][r] = -kInf;
-    float mx = s[0][0];
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const float* p = lp + n * 32 + r4 * 8 + h * 4;
+          const Points pt(px, py, pz, p, p + ROWS, p + 2 * ROWS);
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+          for (int e = 0; e < 4; ++e) {
+            const float r2 = pt.square(e);
+            if constexpr (sizeof(T) == 2)
+              dist[n][r4 * 4 + e] = __builtin_amdgcn_sqrtf(r2);
+            else
+              dist[n][r4 * 4 + e] = dist_of<T>(r2, inv_dist(r2));
+          }
+        }
+    f32x16 s[HB][NS];
+    float mx[HB];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[n][r]);
-    mx = fmaxf(mx, other_half(mx));
-    if (__any(mx > m)) {
-      // a new maximum for some column: what was added so far shrinks
-      const float mn = fmaxf(m, mx);
-      const float f = mn == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-      m = mn;
-      l *= f;
+    for (int hb = 0; hb < HB; ++hb) {
 #pragma unroll
-      for (int b = 0; b < TL::DB; ++b)
+      for (int n = 0; n < NS; ++n) s[hb][n] = TL::dot(lk + n * TL::NP * TL::PART + hb * DP, qf[hb], lane);
+      mx[hb] = -kInf;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[b][r] *= f;
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float x;
+          if constexpr (CAP)
+            x = fmaf(c2, tanh_of<T>(s[hb][n][r] * c1), -m[hb]);
+          else
+            x = fmaf(s[hb][n][r], c1, -m[hb]);
+          if constexpr (BIAS) x = fmaf(-slope[hb], dist[n][r], x);
+          s[hb][n][r] = x;
+        }
     }
-    const float ms = m == -kInf ? 0.f : m;   // nothing seen yet: exp2(-inf) = 0
+    if (edge) {
+      const int last = opaque(vis) - j0;
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
+      for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[n][r] = __builtin_amdgcn_exp2f(s[n][r] - ms);
-        l += s[n][r];
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (n * 32 + acc_row(r, h) >= last) s[hb][n][r] = -kInf;
+    }
+    bool raise = first;
+#pragma unroll
+    for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx[hb] = fmaxf(mx[hb], s[hb][n][r]);
+      mx[hb] = fmaxf(mx[hb], other_half(mx[hb]));
+      raise |= mx[hb] > kSlack;
+    }
+    if (__any(raise)) {
+#pragma unroll
+      for (int hb = 0; hb < HB; ++hb) {
+        const float up = mx[hb] == -kInf ? 0.f : first ? mx[hb] : fmaxf(mx[hb], 0.f), f = __builtin_amdgcn_exp2f(-up);
+        m[hb] += up;
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[hb][n][r] -= up;
+        if (!first) {   // the first tile's factor may be infinite, and meets zeros
+          l[hb] *= f;
+#pragma unroll
+          for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[hb][b][r] *= f;
+        }
       }
-      TL::outer(lv + n * 32 * TL::LD, s[n], o, lane);
     }
+#pragma unroll
+    for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        float sum = 0.f;   // tile by tile, so that a long row's sum rounds less often
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[hb][n][r] = __builtin_amdgcn_exp2f(s[hb][n][r]);
+          sum += s[hb][n][r];
+        }
+        l[hb] += sum;
+        TL::outer(lv + n * TL::NP * TL::PART + hb * DP, s[hb][n], o[hb], lane);
+      }
+  };
+  for (int j0 = kb; j0 < ke; j0 += ROWS * WV::STRIDE) {
+    WV::sync();   // the tile before has been read
+    sk.store(st, lk);
+    sv.store(st, lv);
+    if (BIAS && st < ROWS) lp[st] = sp[0], lp[ROWS + st] = sp[1], lp[2 * ROWS + st] = sp[2];
+    WV::sync();
+    if (j0 + ROWS * WV::STRIDE < ke) fetch(j0 + ROWS * WV::STRIDE);
+
+    tile(__any(j0 + ROWS > vis), j0);
+    first = false;
   }
-  l += other_half(l);
-  if (!live) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const float lse = l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;   // v_log is base 2
-  const size_t orow = qrow * a.hq + head;
-  if (part.splits == 1) {
-    if (h == 0) a.lse[orow] = lse;
-    T* dst = static_cast<T*>(a.out) + orow * a.D;
+
+  float scale[HB], lse[HB];
+#pragma unroll
+  for (int hb = 0; hb < HB; ++hb) {
+    l[hb] += other_half(l[hb]);
+    float top = m[hb], f = 1.f, sum = l[hb];
+    if constexpr (MODE == kRows) {   // the other waves' references and sums
+      float* buf = reinterpret_cast<float*>(lds);
+      __syncthreads();
+      if (h == 0) buf[wv * 64 + lane] = sum == 0.f ? -kInf : top, buf[wv * 64 + 32 + lane] = sum;
+      __syncthreads();
+      top = -kInf;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, buf[k * 64 + lane % 32]);
+      const float ref = top == -kInf ? 0.f : top;
+      f = sum == 0.f ? 0.f : __builtin_amdgcn_exp2f(m[hb] - ref);
+      sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum = fmaf(buf[k * 64 + 32 + lane % 32], __builtin_amdgcn_exp2f(buf[k * 64 + lane % 32] - ref), sum);
+    }
+    scale[hb] = sum == 0.f ? 0.f : f / sum;
+    lse[hb] = sum == 0.f ? -kInf : ln_of(top, __builtin_amdgcn_logf(sum));   // v_log is base 2
 #pragma unroll
     for (int b = 0; b < TL::DB; ++b)
 #pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const int d = b * 32 + r4 * 8 + h * 4;
-        const float x[4] = {o[b][r4 * 4] * inv, o[b][r4 * 4 + 1] * inv, o[b][r4 * 4 + 2] * inv, o[b][r4 * 4 + 3] * inv};
-        if (d < a.D) store_f32<T, 4>(dst + d, x);
-      }
+      for (int r = 0; r < 16; ++r) o[hb][b][r] *= scale[hb];
+  }
+  const size_t rows = (size_t)a.nq * a.hq, row0 = part.splits == 1 ? 0 : w.split * rows;
+  if (live && h == 0 && (MODE != kRows || wv == 0))
+#pragma unroll
+    for (int hb = 0; hb < HB; ++hb)
+      (part.splits == 1 ? a.lse : part.lse)[row0 + qrow * a.hq + head + hb * a.G] = lse[hb];
+  auto put = [&](size_t row, int d, const float* x) {
+    if (part.splits == 1)
+      store_f32<T, 4>(static_cast<T*>(a.out) + row * a.D + d, x);
+    else
+      store_f32<float, 4>(part.o + (row0 + row) * a.D + d, x);
+  };
+  if constexpr (MODE == kRows) {
+    join_waves(reinterpret_cast<float*>(lds), AREA, o, a.D,
+               [&](int c, int hb, int d, const float* x) {
+                 const int cc = w.tile * 32 + c, ii = cc / a.G;
+                 if (ii < w.lq) put((w.q0 + (size_t)ii) * a.hq + (w.head + hb) * a.G + cc % a.G, d, x);
+               });
   } else {
-    const size_t prow = (size_t)w.split * a.nq * a.hq + orow;
-    if (h == 0) part.lse[prow] = lse;
-    float* dst = part.o + prow * a.D;
-#pragma unroll
-    for (int b = 0; b < TL::DB; ++b)
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const int d = b * 32 + r4 * 8 + h * 4;
-        const float x[4] = {o[b][r4 * 4] * inv, o[b][r4 * 4 + 1] * inv, o[b][r4 * 4 + 2] * inv, o[b][r4 * 4 + 3] * inv};
-        if (d < a.D) store_f32<float, 4>(dst + d, x);
-      }
+    each_piece(o, h, a.D, [&](int hb, int d, const float* x) {
+      if (live) put(qrow * a.hq + head + hb * a.G, d, x);
+    });
   }
 }
-
-// ------------------------------------------------- VJP: the scores again --
-
-// From raw products (rows in registers) to P, and for a cap the factor
-// 1 - (t / cap)^2; rx.. are the row-to-column differences' source.
-template <bool CAP>
-__device__ __forceinline__ float score(float u, float c1, float c2, float& th) {
-  float x = u * c1;
-  if constexpr (CAP) {
-    th = tanh_fast(x);
-    x = c2 * th;
-  }
-  return x;
-}
-
-// 1 / r with 0 at r = 0, where the distance has no direction
-__device__ __forceinline__ float inv_dist(float r2) { return r2 > 0.f ? __builtin_amdgcn_rsqf(r2) : 0.f; }
 
 // ------------------------------------------------- VJP: over query columns --
 
 // DELTA: only delta_i = sum_j P dP into part.delta.  Else q_bar, and the
-// position and slope gradients of the query rows into part.row.
-template <class T, int DP, int NW, bool BIAS, bool CAP, bool DELTA>
-__global__ __launch_bounds__(NW * 64) void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
-  using TL = Tile<T, DP>;
-  constexpr int ROWS = 32, COLS = 32 * NW, TH = NW * 64;
-  __shared__ __align__(16) T lk[ROWS * TL::LD];
-  __shared__ __align__(16) T lv[ROWS * TL::LD];
-  __shared__ __align__(16) PosTile<BIAS ? ROWS : 4> lp;
+// position and slope gradients of the query rows into part.row; delta comes
+// from the delta pass, or is <g, out>, formed here and left for the key pass.
+template <class T, int DP, int MODE, bool BIAS, bool CAP, bool DELTA>
+__global__ __launch_bounds__(Waves<MODE>::TH, (waves_per_simd<T, DP, 1, MODE, BIAS>(2, !DELTA, 2 + BIAS, 32)))
+void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
+  using TL = Tile<T, DP, 1>;
+  using WV = Waves<MODE>;
+  constexpr int ROWS = 32;
+  constexpr int AREA = ROWS * TL::LD * TL::NP;   // LDS of one row tile
+  __shared__ __align__(16) bf16 lds[WV::REGIONS * 2 * AREA];
+  __shared__ __align__(16) float lpos[BIAS ? WV::REGIONS * 3 * ROWS : 4];
   const int splits = DELTA ? part.dsplits : part.splits;
-  const Work w = find_work<false>(a, COLS, tiles, splits);
+  const Work w = find_work<false>(a, WV::COLS, 1, tiles, splits);
   if (!w.any) return;
-  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32;
-  const int col = w.tile * COLS + wv * 32 + lane % 32;
+  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32, st = WV::stage_thread();
+  const int col = w.tile * WV::COLS + (MODE == kCols ? wv * 32 : 0) + lane % 32;
   const int i = col / a.G, head = w.head * a.G + col % a.G;
-  const bool live = i < w.lq;
-  const size_t qrow = w.q0 + i, orow = qrow * a.hq + head, nrows = (size_t)a.nq * a.hq;
-  typename TL::Frag qf[TL::STEPS], gf[TL::STEPS];
-  TL::load_cols(static_cast<const T*>(a.q) + (live ? qrow * a.qs + (size_t)head * a.D : 0), live, a.D, h, qf);
-  TL::load_cols(static_cast<const T*>(a.g) + (live ? orow * a.D : 0), live, a.D, h, gf);
-  float px = 0.f, py = 0.f, pz = 0.f, slope = 0.f;
-  if (BIAS && live) {
-    px = a.pos_q[3 * qrow], py = a.pos_q[3 * qrow + 1], pz = a.pos_q[3 * qrow + 2];
-    slope = a.slope[head] * kLog2e;
-  }
+  const bool live = i < w.lq, lead = live && h == 0 && (MODE != kRows || wv == 0);
+  const size_t qrow = w.q0 + i, nrows = (size_t)a.nq * a.hq;
+  bf16 *lk = lds + WV::region() * 2 * AREA, *lv = lk + AREA;
+  float* lp = lpos + (BIAS ? WV::region() * 3 * ROWS : 0);
+
   const int vis = live ? visible(a, w, i) : 0;
-  // an empty row has lse = -inf; +inf makes its P vanish
-  float lse = live ? a.lse[orow] * kLog2e : kInf;
-  if (lse == -kInf) lse = kInf;
-  float delta = 0.f;
-  if (!DELTA && live)
-    for (int s = 0; s < part.dsplits; ++s) delta += part.delta[(size_t)s * nrows + orow];
-  const int iend = min(w.lq, (w.tile * COLS + COLS - 1) / a.G + 1);
+  const int iend = min(w.lq, (w.tile * WV::COLS + WV::COLS - 1) / a.G + 1);
   int kb, ke;
   split_range(visible(a, w, iend - 1), ROWS, splits, w.split, kb, ke);
-  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+  if (MODE == kRows) kb += wv * ROWS;
 
-  f32x16 dq[TL::DB];
-#pragma unroll
-  for (int b = 0; b < TL::DB; ++b) dq[b] = f32x16{};
-  float gx = 0.f, gy = 0.f, gz = 0.f, gs = 0.f, dsum = 0.f;
-
-  Stage<T, DP, ROWS, TH> sk, sv;
-  float sp[3] = {0.f, 0.f, 0.f};
+  Stage<T, DP, 1, ROWS, WV::STAGE> sk, sv;
+  const uint32_t place = sk.place(st, a.D, a.D);
+  float sp[3];
   const T* kbase = static_cast<const T*>(a.k) + (size_t)w.k0 * a.ks + (size_t)w.head * a.D;
   const T* vbase = static_cast<const T*>(a.v) + (size_t)w.k0 * a.vs + (size_t)w.head * a.D;
+  const uint32_t kst = (uint32_t)a.ks * sizeof(T), vst = (uint32_t)a.vs * sizeof(T);
+  const int row_bytes = a.D * (int)sizeof(T);
   auto fetch = [&](int j0) {
-    sk.load(a.D, [&](int r) { return j0 + r < ke ? kbase + (size_t)(j0 + r) * a.ks : nullptr; });
-    sv.load(a.D, [&](int r) { return j0 + r < ke ? vbase + (size_t)(j0 + r) * a.vs : nullptr; });
-    if (BIAS && threadIdx.x < ROWS)
+    sk.load(make_rsrc(kbase + (size_t)j0 * a.ks, reach(j0, w.lk, kst, row_bytes)), st, place,
+            [&](int r) { return r * kst; });
+    sv.load(make_rsrc(vbase + (size_t)j0 * a.vs, reach(j0, w.lk, vst, row_bytes)), st, place,
+            [&](int r) { return r * vst; });
+    if constexpr (BIAS) {
+      const auto buf = make_rsrc(a.pos_k + 3 * (size_t)(w.k0 + j0), reach(j0, w.lk, 12, 12));
 #pragma unroll
       for (int c = 0; c < 3; ++c)
-        sp[c] = j0 + (int)threadIdx.x < ke ? a.pos_k[3 * (size_t)(w.k0 + j0 + threadIdx.x) + c] : 0.f;
+        sp[c] = buf_load(buf, st < ROWS ? st * 12 + c * 4 : kNowhere, 0);
+    }
   };
   if (kb < ke) fetch(kb);
-  for (int j0 = kb; j0 < ke; j0 += ROWS) {
-    __syncthreads();
-    sk.store(lk);
-    sv.store(lv);
-    if (BIAS && threadIdx.x < ROWS) lp.x[threadIdx.x] = sp[0], lp.y[threadIdx.x] = sp[1], lp.z[threadIdx.x] = sp[2];
-    __syncthreads();
-    if (j0 + ROWS < ke) fetch(j0 + ROWS);
 
+  typename TL::Cols qf, gf;
+  f32x16 dq[1][TL::DB];
+  const size_t orow = qrow * a.hq + head;
+  TL::load_cols(static_cast<const T*>(a.q) + (live ? qrow * a.qs + (size_t)head * a.D : 0), live, a.D, h, qf);
+  TL::load_cols(static_cast<const T*>(a.g) + (live ? orow * a.D : 0), live, a.D, h, gf);
+  const float slope = BIAS && live ? a.slope[head] * kLog2e : 0.f;
+  const Norm norm(live ? a.lse[orow] : -kInf);   // the factor is the column's own: at the end
+  float delta = 0.f;
+  if constexpr (!DELTA) {
+    if (part.exact) {
+      if (live)
+        for (int s = 0; s < part.dsplits; ++s) delta += part.delta[s * nrows + orow];
+    } else {
+      // the lane's elements of both rows, as load_cols takes them
+      for (int d = 8 * h; live && d < a.D; d += 16) {
+        float x[8], y[8];
+        load_f32<T, 8>(static_cast<const T*>(a.out) + orow * a.D + d, x);
+        load_f32<T, 8>(static_cast<const T*>(a.g) + orow * a.D + d, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+      }
+      delta += other_half(delta);
+      if (lead && w.split == 0) part.delta[orow] = delta;
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < TL::DB; ++b) dq[0][b] = f32x16{};
+  float px = 0.f, py = 0.f, pz = 0.f;
+  if (BIAS && live) px = a.pos_q[3 * qrow], py = a.pos_q[3 * qrow + 1], pz = a.pos_q[3 * qrow + 2];
+  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+  float v[4] = {0.f, 0.f, 0.f, 0.f}, dsum[1] = {0.f};   // position and slope gradients; delta
+
+  auto tile = [&](bool edge, int j0) {
+    float gp[3] = {0.f, 0.f, 0.f}, gs = 0.f, gd = 0.f;   // of this tile: long sums round less often
     f32x16 s = TL::dot(lk, qf, lane);
     const f32x16 dp = TL::dot(lv, gf, lane);
-    const bool edge = __any(j0 + ROWS > vis);
+    if (edge && !CAP) {
+      const int last = opaque(vis) - j0;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (acc_row(r, h) >= last) s[r] = -kInf;
+    }
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
-      f32x4 kx, ky, kz;
-      if constexpr (BIAS) {
-        const int j = r4 * 8 + h * 4;
-        kx = four(lp.x + j), ky = four(lp.y + j), kz = four(lp.z + j);
-      }
+      const float* p = lp + (BIAS ? r4 * 8 + h * 4 : 0);
+      const Points pt(px, py, pz, p, BIAS ? p + ROWS : p, BIAS ? p + 2 * ROWS : p);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = r4 * 4 + e;
-        float th = 0.f, x = score<CAP>(s[r], c1, c2, th);
-        float dx, dy, dz, dist, inv;
-        if constexpr (BIAS) {
-          dx = px - kx[e], dy = py - ky[e], dz = pz - kz[e];
-          const float r2 = fmaf(dx, dx, fmaf(dy, dy, dz * dz));
-          inv = inv_dist(r2);
-          dist = r2 * inv;
-          x = fmaf(-slope, dist, x);
-        }
-        if (edge && j0 + acc_row(r, h) >= vis) x = -kInf;
-        const float p = __builtin_amdgcn_exp2f(x - lse);
-        if constexpr (DELTA) {
-          dsum = fmaf(p, dp[r], dsum);
+        float th = 0.f, x, inv, d;
+        if constexpr (CAP) {
+          th = tanh_of<T>(s[r] * c1);
+          x = fmaf(c2, th, -norm.ref);
+          if (edge && j0 + acc_row(r, h) >= vis) x = -kInf;
         } else {
-          float ds = p * (dp[r] - delta);
+          x = fmaf(s[r], c1, -norm.ref);
+        }
+        if constexpr (BIAS) {
+          inv = inv_dist(pt.square(e));
+          d = dist_of<T>(pt.square(e), inv);
+          x = fmaf(-slope, d, x);
+        }
+        const float pr = __builtin_amdgcn_exp2f(x);
+        if constexpr (DELTA) {
+          gd = fmaf(pr, dp[r], gd);
+        } else {
+          float ds = pr * (dp[r] - delta);
           if constexpr (BIAS) {
-            gs = fmaf(ds, dist, gs);
-            const float f = ds * inv;
-            gx = fmaf(f, dx, gx), gy = fmaf(f, dy, gy), gz = fmaf(f, dz, gz);
+            gs = fmaf(ds, d, gs);
+            pt.add(e, ds * inv, gp);   // the slope is the column's own: at the end
           }
-          if constexpr (CAP) ds *= 1.f - th * th;
+          if constexpr (CAP) ds = fmaf(-th * th, ds, ds);
           s[r] = ds;
         }
       }
     }
-    if constexpr (!DELTA) TL::outer(lk, s, dq, lane);
+    if constexpr (DELTA) dsum[0] += gd;
+    if constexpr (BIAS && !DELTA) v[0] += gp[0], v[1] += gp[1], v[2] += gp[2], v[3] += gs;
+    if constexpr (!DELTA) TL::outer(lk, s, dq[0], lane);
+  };
+  for (int j0 = kb; j0 < ke; j0 += ROWS * WV::STRIDE) {
+    WV::sync();
+    sk.store(st, lk);
+    sv.store(st, lv);
+    if (BIAS && st < ROWS) lp[st] = sp[0], lp[ROWS + st] = sp[1], lp[2 * ROWS + st] = sp[2];
+    WV::sync();
+    if (j0 + ROWS * WV::STRIDE < ke) fetch(j0 + ROWS * WV::STRIDE);
+
+    tile(__any(j0 + ROWS > vis), j0);
   }
+  float* slices = reinterpret_cast<float*>(lds);
+  constexpr int slice = AREA;
   if constexpr (DELTA) {
-    dsum += other_half(dsum);
-    if (live && h == 0) part.delta[(size_t)w.split * nrows + orow] = dsum;
+    dsum[0] = (dsum[0] + other_half(dsum[0])) * norm.factor;
+    if constexpr (MODE == kRows) join_values(slices, dsum);
+    if (lead) part.delta[w.split * nrows + orow] = dsum[0];
     return;
   }
   if constexpr (BIAS) {
-    gx += other_half(gx), gy += other_half(gy), gz += other_half(gz), gs += other_half(gs);
-    if (part.row && live && h == 0) {
-      const float t = -slope * kLn2;
-      const float x[4] = {t * gx, t * gy, t * gz, -gs};
-      store_f32<float, 4>(part.row + ((size_t)w.split * nrows + orow) * 4, x);
-    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = (v[c] + other_half(v[c])) * norm.factor;
+    if constexpr (MODE == kRows) join_values(slices, v);
+    const float t = -kLn2 * slope, x[4] = {t * v[0], t * v[1], t * v[2], -v[3]};
+    if (lead) store_f32<float, 4>(part.row + (w.split * nrows + orow) * 4, x);
   }
-  if (!live || !a.gq) return;
+  if (!a.gq) return;   // the whole launch
 #pragma unroll
   for (int b = 0; b < TL::DB; ++b)
 #pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
-      const int d = b * 32 + r4 * 8 + h * 4;
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = dq[b][r4 * 4 + e] * a.scale;
-      if (d >= a.D) continue;
-      if (part.splits == 1)
-        store_f32<T, 4>(static_cast<T*>(a.gq) + orow * a.D + d, x);
-      else
-        store_f32<float, 4>(part.o + ((size_t)w.split * nrows + orow) * a.D + d, x);
-    }
+    for (int r = 0; r < 16; ++r) dq[0][b][r] *= norm.factor;
+  auto put = [&](size_t row, int d, const float* x) {
+    const float y[4] = {x[0] * a.scale, x[1] * a.scale, x[2] * a.scale, x[3] * a.scale};
+    if (part.splits == 1)
+      store_f32<T, 4>(static_cast<T*>(a.gq) + row * a.D + d, y);
+    else
+      store_f32<float, 4>(part.o + (w.split * nrows + row) * a.D + d, y);
+  };
+  if constexpr (MODE == kRows) {
+    join_waves(slices, slice, dq, a.D, [&](int c, int, int d, const float* x) {
+      const int cc = w.tile * 32 + c, ii = cc / a.G;
+      if (ii < w.lq) put((w.q0 + (size_t)ii) * a.hq + w.head * a.G + cc % a.G, d, x);
+    });
+  } else {
+    each_piece(dq, h, a.D, [&](int, int d, const float* x) {
+      if (live) put(orow, d, x);
+    });
+  }
 }
 
 // --------------------------------------------------- VJP: over key columns --
 
-template <int ROWS>
+// What a row tile of packed queries carries besides q and g.
+template <int ROWS, bool BIAS>
 struct QueryTile {
-  float lse[ROWS], delta[ROWS];
+  float ref[ROWS], factor[ROWS], delta[ROWS];
   int vis[ROWS];
-};
-template <int ROWS>
-struct QueryPos {
-  float x[ROWS], y[ROWS], z[ROWS], slope[ROWS];
+  float pos[BIAS ? 3 : 1][BIAS ? ROWS : 4], slope[BIAS ? ROWS : 4];
 };
 
-template <class T, int DP, int NW, bool BIAS, bool CAP>
-__global__ __launch_bounds__(NW * 64) void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
-  using TL = Tile<T, DP>;
-  constexpr int ROWS = 32, COLS = 32 * NW, TH = NW * 64;
-  __shared__ __align__(16) T lq[ROWS * TL::LD];
-  __shared__ __align__(16) T lg[ROWS * TL::LD];
-  __shared__ __align__(16) QueryTile<ROWS> lr;
-  __shared__ __align__(16) QueryPos<BIAS ? ROWS : 4> lp;
-  const Work w = find_work<true>(a, COLS, tiles, part.splits);
+template <class T, int DP, int MODE, bool BIAS, bool CAP>
+__global__ __launch_bounds__(Waves<MODE>::TH, (waves_per_simd<T, DP, 1, MODE, BIAS>(2, 2, 2 + BIAS, 32)))
+void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
+  using TL = Tile<T, DP, 1>;
+  using WV = Waves<MODE>;
+  constexpr int ROWS = 32;
+  constexpr int AREA = ROWS * TL::LD * TL::NP;   // LDS of one row tile
+  __shared__ __align__(16) bf16 lds[WV::REGIONS * 2 * AREA];
+  __shared__ __align__(16) QueryTile<ROWS, BIAS> lrow[WV::REGIONS];
+  const Work w = find_work<true>(a, WV::COLS, 1, tiles, part.splits);
   if (!w.any) return;
-  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32;
-  const int j = w.tile * COLS + wv * 32 + lane % 32;
+  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32, st = WV::stage_thread();
+  const int j = w.tile * WV::COLS + (MODE == kCols ? wv * 32 : 0) + lane % 32;
   const bool live = j < w.lk;
   const size_t krow = w.k0 + j, nrows = (size_t)a.nq * a.hq;
-  typename TL::Frag kf[TL::STEPS], vf[TL::STEPS];
-  TL::load_cols(static_cast<const T*>(a.k) + (live ? krow * a.ks + (size_t)w.head * a.D : 0), live, a.D, h, kf);
-  TL::load_cols(static_cast<const T*>(a.v) + (live ? krow * a.vs + (size_t)w.head * a.D : 0), live, a.D, h, vf);
-  float px = 0.f, py = 0.f, pz = 0.f;
-  if (BIAS && live) px = a.pos_k[3 * krow], py = a.pos_k[3 * krow + 1], pz = a.pos_k[3 * krow + 2];
-  // packed query rows [rb, re): those before the first that sees the block's
-  // first key are left out
-  const int j0 = w.tile * COLS;
-  const int i0 = a.causal && j0 >= w.pre ? min(w.lq, max(0, j0 - (w.lk - w.lq))) : 0;
-  const int rows = (w.lq - i0) * a.G;
+  bf16 *lq = lds + WV::region() * 2 * AREA, *lg = lq + AREA;
+  QueryTile<ROWS, BIAS>& lr = lrow[WV::region()];
+
+  // Packed query rows [rb, re): those before the first that sees the block's
+  // first key are left out.  A tile holds whole queries (all G heads) where
+  // G <= 32, so that its rows lie the same way in every tile.
+  const int jfirst = w.tile * WV::COLS, step = a.G <= ROWS ? ROWS / a.G * a.G : ROWS;
+  const int i0 = a.causal && jfirst >= w.pre ? min(w.lq, max(0, jfirst - (w.lk - w.lq))) : 0;
   int rb, re;
-  split_range(rows, ROWS, part.splits, w.split, rb, re);
+  split_range((w.lq - i0) * a.G, step, part.splits, w.split, rb, re);
   rb += i0 * a.G, re += i0 * a.G;
-  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+  if (MODE == kRows) rb += wv * step;
 
-  f32x16 dk[TL::DB], dv[TL::DB];
-#pragma unroll
-  for (int b = 0; b < TL::DB; ++b) dk[b] = f32x16{}, dv[b] = f32x16{};
-  float gx = 0.f, gy = 0.f, gz = 0.f;
-
-  Stage<T, DP, ROWS, TH> sq, sg;
-  float s_lse = kInf, s_delta = 0.f, sp[4] = {0.f, 0.f, 0.f, 0.f};
-  int s_vis = 0;
+  using ST = Stage<T, DP, 1, ROWS, WV::STAGE>;
+  ST sq, sg;
+  const uint32_t place = ST::place(st, a.D, a.G * a.D);
+  float s_lse, s_delta, s_slope = 0.f, sp[3] = {0.f, 0.f, 0.f};
+  int s_vis;
   const T* qbase = static_cast<const T*>(a.q) + (size_t)w.q0 * a.qs + (size_t)w.head * a.G * a.D;
   const T* gbase = static_cast<const T*>(a.g) + ((size_t)w.q0 * a.hq + (size_t)w.head * a.G) * a.D;
+  const uint32_t qst = (uint32_t)a.qs * sizeof(T), gst = (uint32_t)(a.hq * a.D) * sizeof(T);
+  const int row_bytes = a.G * a.D * (int)sizeof(T), head_bytes = a.D * (int)sizeof(T);
+  uint32_t qoff[ST::N], goff[ST::N];
+  int mi, mg;
+  // rows of a tile that starts at head `rem` of a query
+  auto lay_out = [&](int rem) {
+    auto at = [&](int r, int& i, int& g) {
+      i = a.G <= ROWS ? r / a.G : rem + r >= a.G;
+      g = rem + r - i * a.G;
+    };
+#pragma unroll
+    for (int n = 0; n < ST::N; ++n) {
+      const int r = st / TL::CPR + n * ST::STEP;
+      int i, g;
+      at(r, i, g);
+      const uint32_t p = r < step ? place : kNowhere;
+      qoff[n] = p + i * qst + g * head_bytes;
+      goff[n] = p + i * gst + g * head_bytes;
+    }
+    at(st % ROWS, mi, mg);   // the thread's row of the small values
+  };
+  lay_out(0);
   auto fetch = [&](int r0) {
-    sq.load(a.D, [&](int r) {
-      const int c = r0 + r, i = c / a.G;
-      return c < re ? qbase + (size_t)i * a.qs + (size_t)(c - i * a.G) * a.D : nullptr;
-    });
-    sg.load(a.D, [&](int r) {
-      const int c = r0 + r, i = c / a.G;
-      return c < re ? gbase + ((size_t)i * a.hq + (c - i * a.G)) * a.D : nullptr;
-    });
-    if (threadIdx.x < ROWS) {
-      const int c = r0 + threadIdx.x, i = c / a.G, head = w.head * a.G + (c - i * a.G);
-      const bool on = c < re;
+    const int ib = r0 / a.G;
+    if (a.G > ROWS) lay_out(r0 - ib * a.G);
+    sq.load(make_rsrc(qbase + (size_t)ib * a.qs, reach(ib, w.lq, qst, row_bytes)), qoff);
+    sg.load(make_rsrc(gbase + (size_t)ib * a.hq * a.D, reach(ib, w.lq, gst, row_bytes)), goff);
+    if (st < ROWS) {
+      const int i = ib + mi, head = w.head * a.G + mg;
+      const bool on = st < step && r0 + st < re;
       const size_t orow = (size_t)(w.q0 + i) * a.hq + head;
-      s_lse = on ? a.lse[orow] * kLog2e : kInf;
-      if (s_lse == -kInf) s_lse = kInf;   // an empty row: P = 0
-      s_delta = 0.f;
-      if (on)
-        for (int s = 0; s < part.dsplits; ++s) s_delta += part.delta[(size_t)s * nrows + orow];
+      s_lse = on ? a.lse[orow] : -kInf;
+      s_delta = on ? part.delta[orow] : 0.f;
+      for (int s = 1; s < part.dsplits; ++s) s_delta += on ? part.delta[s * nrows + orow] : 0.f;
       s_vis = on ? visible(a, w, i) : 0;
       if constexpr (BIAS) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) sp[k] = on ? a.pos_q[3 * (size_t)(w.q0 + i) + k] : 0.f;
-        sp[3] = on ? a.slope[head] * kLog2e : 0.f;
+        s_slope = on ? a.slope[head] * kLog2e : 0.f;
       }
     }
   };
   if (rb < re) fetch(rb);
-  for (int r0 = rb; r0 < re; r0 += ROWS) {
-    __syncthreads();
-    sq.store(lq);
-    sg.store(lg);
-    if (threadIdx.x < ROWS) {
-      lr.lse[threadIdx.x] = s_lse, lr.delta[threadIdx.x] = s_delta, lr.vis[threadIdx.x] = s_vis;
-      if constexpr (BIAS)
-        lp.x[threadIdx.x] = sp[0], lp.y[threadIdx.x] = sp[1], lp.z[threadIdx.x] = sp[2], lp.slope[threadIdx.x] = sp[3];
-    }
-    __syncthreads();
-    if (r0 + ROWS < re) fetch(r0 + ROWS);
 
+  typename TL::Cols kf, vf;
+  f32x16 dk[1][TL::DB], dv[1][TL::DB];
+  TL::load_cols(static_cast<const T*>(a.k) + (live ? krow * a.ks + (size_t)w.head * a.D : 0), live, a.D, h, kf);
+  TL::load_cols(static_cast<const T*>(a.v) + (live ? krow * a.vs + (size_t)w.head * a.D : 0), live, a.D, h, vf);
+#pragma unroll
+  for (int b = 0; b < TL::DB; ++b) dk[0][b] = f32x16{}, dv[0][b] = f32x16{};
+  float px = 0.f, py = 0.f, pz = 0.f;
+  if (BIAS && live) px = a.pos_k[3 * krow], py = a.pos_k[3 * krow + 1], pz = a.pos_k[3 * krow + 2];
+  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+  float gp[3] = {0.f, 0.f, 0.f};
+
+  auto tile = [&](bool edge) {
+    float gt[3] = {0.f, 0.f, 0.f};   // of this tile
     f32x16 s = TL::dot(lq, kf, lane);
     f32x16 dp = TL::dot(lg, vf, lane);
+    if (edge && !CAP) {
+      const int jj = opaque(j);
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const i32x4 vis = *reinterpret_cast<const i32x4*>(lr.vis + r4 * 8 + h * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (jj >= vis[e]) s[r4 * 4 + e] = -kInf;
+      }
+    }
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
-      const int rr = r4 * 8 + h * 4;
-      const f32x4 lse = four(lr.lse + rr), delta = four(lr.delta + rr);
-      const i32x4 vis = *reinterpret_cast<const i32x4*>(lr.vis + rr);
-      f32x4 qx, qy, qz, sl;
-      if constexpr (BIAS) qx = four(lp.x + rr), qy = four(lp.y + rr), qz = four(lp.z + rr), sl = four(lp.slope + rr);
+      const int rr = r4 * 8 + h * 4, pp = BIAS ? rr : 0;
+      const f32x4 ref = four(lr.ref + rr), factor = four(lr.factor + rr), delta = four(lr.delta + rr);
+      i32x4 vis;
+      if constexpr (CAP) vis = *reinterpret_cast<const i32x4*>(lr.vis + rr);
+      const Points pt(px, py, pz, lr.pos[0] + pp, lr.pos[BIAS ? 1 : 0] + pp, lr.pos[BIAS ? 2 : 0] + pp);
+      f32x4 sl;
+      if constexpr (BIAS) sl = four(lr.slope + rr);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = r4 * 4 + e;
-        float th = 0.f, x = score<CAP>(s[r], c1, c2, th);
-        float dx, dy, dz, inv;
-        if constexpr (BIAS) {
-          dx = px - qx[e], dy = py - qy[e], dz = pz - qz[e];
-          const float r2 = fmaf(dx, dx, fmaf(dy, dy, dz * dz));
-          inv = inv_dist(r2);
-          x = fmaf(-sl[e], r2 * inv, x);
+        float th = 0.f, x, inv;
+        if constexpr (CAP) {
+          th = tanh_of<T>(s[r] * c1);
+          x = fmaf(c2, th, -ref[e]);
+          if (edge && j >= vis[e]) x = -kInf;
+        } else {
+          x = fmaf(s[r], c1, -ref[e]);
         }
-        if (j >= vis[e]) x = -kInf;
-        const float p = __builtin_amdgcn_exp2f(x - lse[e]);
+        if constexpr (BIAS) {
+          inv = inv_dist(pt.square(e));
+          x = fmaf(-sl[e], dist_of<T>(pt.square(e), inv), x);
+        }
+        const float p = __builtin_amdgcn_exp2f(x) * factor[e];
         float ds = p * (dp[r] - delta[e]);
-        if constexpr (BIAS) {
-          const float f = ds * inv * sl[e];
-          gx = fmaf(f, dx, gx), gy = fmaf(f, dy, gy), gz = fmaf(f, dz, gz);
-        }
-        if constexpr (CAP) ds *= 1.f - th * th;
+        if constexpr (BIAS) pt.add(e, ds * inv * sl[e], gt);
+        if constexpr (CAP) ds = fmaf(-th * th, ds, ds);
         s[r] = p;
         dp[r] = ds;
       }
     }
-    TL::outer(lg, s, dv, lane);
-    TL::outer(lq, dp, dk, lane);
+    if constexpr (BIAS) gp[0] += gt[0], gp[1] += gt[1], gp[2] += gt[2];
+    TL::outer(lg, s, dv[0], lane);
+    TL::outer(lq, dp, dk[0], lane);
+  };
+  for (int r0 = rb; r0 < re; r0 += step * WV::STRIDE) {
+    WV::sync();
+    sq.store(st, lq);
+    sg.store(st, lg);
+    if (st < ROWS) {
+      const Norm norm(s_lse);
+      lr.ref[st] = norm.ref;
+      lr.factor[st] = norm.factor;
+      lr.delta[st] = s_delta;
+      lr.vis[st] = s_vis;
+      if constexpr (BIAS) lr.pos[0][st] = sp[0], lr.pos[1][st] = sp[1], lr.pos[2][st] = sp[2], lr.slope[st] = s_slope;
+    }
+    WV::sync();
+    // the tile's first row sees the least; absent rows see nothing
+    const int s_least = step < ROWS || r0 + ROWS > re ? 0 : lr.vis[0];
+    if (r0 + step * WV::STRIDE < re) fetch(r0 + step * WV::STRIDE);
+
+    tile(__any(j >= s_least));
   }
-  const size_t orow = krow * a.hk + w.head, knum = (size_t)a.nk * a.hk;
+  const size_t knum = (size_t)a.nk * a.hk;
+  float* slices = reinterpret_cast<float*>(lds);
+  constexpr int slice = AREA;
   if constexpr (BIAS) {
-    gx += other_half(gx), gy += other_half(gy), gz += other_half(gz);
-    if (part.col && live && h == 0) {
-      const float x[4] = {-kLn2 * gx, -kLn2 * gy, -kLn2 * gz, 0.f};
-      store_f32<float, 4>(part.col + ((size_t)w.split * knum + orow) * 4, x);
-    }
+#pragma unroll
+    for (int c = 0; c < 3; ++c) gp[c] += other_half(gp[c]);
+    if constexpr (MODE == kRows) join_values(slices, gp);
+    const float x[4] = {-kLn2 * gp[0], -kLn2 * gp[1], -kLn2 * gp[2], 0.f};
+    if (live && h == 0 && (MODE != kRows || wv == 0))
+      store_f32<float, 4>(part.col + (w.split * knum + krow * a.hk + w.head) * 4, x);
   }
-  if (!live) return;
-#pragma unroll
-  for (int b = 0; b < TL::DB; ++b)
-#pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
-      const int d = b * 32 + r4 * 8 + h * 4;
-      if (d >= a.D) continue;
-      float x[4], y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = dk[b][r4 * 4 + e] * a.scale, y[e] = dv[b][r4 * 4 + e];
-      if (part.splits == 1) {
-        if (a.gk) store_f32<T, 4>(static_cast<T*>(a.gk) + orow * a.D + d, x);
-        if (a.gv) store_f32<T, 4>(static_cast<T*>(a.gv) + orow * a.D + d, y);
-      } else {
-        const size_t at = ((size_t)w.split * knum + orow) * a.D + d;
-        if (a.gk) store_f32<float, 4>(part.o + at, x);
-        if (a.gv) store_f32<float, 4>(part.o2 + at, y);
-      }
+  auto put = [&](T* out, float* split, float f, size_t row, int d, const float* x) {
+    const float y[4] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f};
+    if (part.splits == 1)
+      store_f32<T, 4>(out + row * a.D + d, y);
+    else
+      store_f32<float, 4>(split + (w.split * knum + row) * a.D + d, y);
+  };
+  auto write = [&](const f32x16 (&o)[1][TL::DB], void* out, float* split, float f) {
+    if (!out) return;   // the whole launch
+    if constexpr (MODE == kRows) {
+      join_waves(slices, slice, o, a.D, [&](int c, int, int d, const float* x) {
+        const int jj = w.tile * 32 + c;
+        if (jj < w.lk) put(static_cast<T*>(out), split, f, (w.k0 + (size_t)jj) * a.hk + w.head, d, x);
+      });
+    } else {
+      each_piece(o, h, a.D, [&](int, int d, const float* x) {
+        if (live) put(static_cast<T*>(out), split, f, krow * a.hk + w.head, d, x);
+      });
     }
+  };
+  write(dk, a.gk, part.o, a.scale);
+  write(dv, a.gv, part.o2, 1.f);
 }
 
 // ---------------------------------------------------------------- launches --
 
-template <class T, int DP, int NW>
-void attn_launch_nw(const AttnLaunch& l, const AttnArgs& a, const AttnPart& p, hipStream_t st) {
-  constexpr int NS = sizeof(T) == 2 ? 2 : 1;
-  const bool keys = l.pass == kAttnKey;
+template <class T, int DP, int HB, int MODE, bool BIAS, bool CAP>
+void attn_launch_one(const AttnLaunch& l, const AttnArgs& a, const AttnPart& p, hipStream_t st) {
   const int splits = l.pass == kAttnDelta ? p.dsplits : p.splits;
-  const int64_t cols = 32 * NW;
-  const int tiles = (int)((keys ? (int64_t)a.nk : (int64_t)a.nq * a.G) / cols + a.S);
-  const int64_t units = (int64_t)a.hk * splits;
-  int64_t blocks;
-  if (units % 8 == 0)
-    blocks = units * tiles;
-  else if (8 % units == 0)
-    blocks = 8 * ((tiles + 8 / units - 1) / (8 / units));
-  else
-    blocks = units * tiles;
-  const dim3 grid((unsigned)blocks), block(NW * 64);
-  auto go = [&](auto bias, auto cap) {
-    constexpr bool B = decltype(bias)::value, C = decltype(cap)::value;
-    switch (l.pass) {
-      case kAttnFwd: hipLaunchKernelGGL((attn_fwd_kernel<T, DP, NW, NS, B, C>), grid, block, 0, st, a, p, tiles); break;
-      case kAttnDelta:
-        if constexpr (sizeof(T) == 2 && B)   // fp32 rows take delta from out
-          hipLaunchKernelGGL((attn_query_kernel<T, DP, NW, B, C, true>), grid, block, 0, st, a, p, tiles);
-        break;
-      case kAttnQuery:
-        hipLaunchKernelGGL((attn_query_kernel<T, DP, NW, B, C, false>), grid, block, 0, st, a, p, tiles);
-        break;
-      default: hipLaunchKernelGGL((attn_key_kernel<T, DP, NW, B, C>), grid, block, 0, st, a, p, tiles); break;
+  const int64_t cols = Waves<MODE>::COLS;
+  const int tiles = (int)((l.pass == kAttnKey ? (int64_t)a.nk : (int64_t)a.nq * a.G) / cols + a.S);
+  const int64_t units = (int64_t)(a.hk / HB) * splits;
+  const int64_t blocks =
+      8 % units == 0 ? 8 * ((tiles + 8 / units - 1) / (8 / units)) : units * tiles;
+  const dim3 grid((unsigned)blocks), block(Waves<MODE>::TH);
+  switch (l.pass) {
+    case kAttnFwd: hipLaunchKernelGGL((attn_fwd_kernel<T, DP, HB, MODE, BIAS, CAP>), grid, block, 0, st, a, p, tiles); break;
+    case kAttnDelta:
+      if constexpr (sizeof(T) == 2 && BIAS && HB == 1)   // fp32: delta from out
+        hipLaunchKernelGGL((attn_query_kernel<T, DP, MODE, BIAS, CAP, true>), grid, block, 0, st, a, p, tiles);
+      break;
+    case kAttnQuery:
+      if constexpr (HB == 1)
+        hipLaunchKernelGGL((attn_query_kernel<T, DP, MODE, BIAS, CAP, false>), grid, block, 0, st, a, p, tiles);
+      break;
+    default:
+      if constexpr (HB == 1)
+        hipLaunchKernelGGL((attn_key_kernel<T, DP, MODE, BIAS, CAP>), grid, block, 0, st, a, p, tiles);
+      break;
+  }
+}
+
+template <class T, int DP, int HB, bool BIAS>
+void attn_launch_bias(const AttnLaunch& l, const AttnArgs& a, const AttnPart& p, hipStream_t st) {
+  auto mode = [&](auto cap) {
+    constexpr bool C = decltype(cap)::value;
+    if constexpr (attn_cols_only(sizeof(T) == 2, DP)) {
+      attn_launch_one<T, DP, HB, kCols, BIAS, C>(l, a, p, st);
+    } else {
+      switch (l.mode) {
+        case kOne: attn_launch_one<T, DP, HB, kOne, BIAS, C>(l, a, p, st); break;
+        case kCols: attn_launch_one<T, DP, HB, kCols, BIAS, C>(l, a, p, st); break;
+        default: attn_launch_one<T, DP, HB, kRows, BIAS, C>(l, a, p, st); break;
+      }
     }
   };
-  using Yes = std::integral_constant<bool, true>;
-  using No = std::integral_constant<bool, false>;
-  if (a.slope)
-    a.cap > 0.f ? go(Yes{}, Yes{}) : go(Yes{}, No{});
-  else
-    a.cap > 0.f ? go(No{}, Yes{}) : go(No{}, No{});
+  a.cap > 0.f ? mode(std::integral_constant<bool, true>{}) : mode(std::integral_constant<bool, false>{});
 }
 
 template <class T, int DP>
 void attn_launch(const AttnLaunch& l, const AttnArgs& a, const AttnPart& p, hipStream_t st) {
-  l.waves == 1 ? attn_launch_nw<T, DP, 1>(l, a, p, st) : attn_launch_nw<T, DP, 4>(l, a, p, st);
+  if (!a.slope)
+    attn_launch_bias<T, DP, 1, false>(l, a, p, st);
+  else if (l.hb == 1)
+    attn_launch_bias<T, DP, 1, true>(l, a, p, st);
+  else if constexpr (attn_two_heads(sizeof(T) == 2, DP))
+    attn_launch_bias<T, DP, 2, true>(l, a, p, st);
 }
 
 }  // namespace fc

@@ -581,7 +581,7 @@ fc_status fc_qk_norm_rope_vjp(const fc_qk_rope_desc* d, const void* q, const voi
  * Requirements: n_query, n_key >= 0, n_segments >= 1, heads_k >= 1,
  * heads_q <= 256 a multiple of heads_k, head_dim a multiple of 8 and <= 128,
  * scale > 0, cap >= 0; q, k, v, out, g_out and their gradients 16-byte
- * aligned with strides of whole 16-byte pieces.
+ * aligned with strides of whole 16-byte pieces, at most 2^22 elements.
  * Values inside a segment must be finite, also those a causal mask hides;
  * rows behind the last segment may hold anything: they are not read, and
  * their outputs and gradients are left as they were.
