@@ -63,44 +63,49 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(int n, int width, int S, 
   store_f32<T, 4>(out + at, x);
 }
 
-// position gradient of a row: its heads and splits in order; `self` adds the
-// part it has as a key
-__global__ __launch_bounds__(256) void attn_pos_kernel(int n, int S, const int* seg, int h0, int s0,
-                                                       const float* __restrict__ p0, int h1, int s1,
-                                                       const float* __restrict__ p1, float* __restrict__ out) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= n || !in_segments(seg, S, n, i)) return;
-  float x = 0.f, y = 0.f, z = 0.f;
-  auto add = [&](int H, int splits, const float* part) {
-    for (int s = 0; s < splits; ++s)
-      for (int h = 0; h < H; ++h) {
-        float v[4];
-        load_f32<float, 4>(part + (((size_t)s * n + i) * H + h) * 4, v);
-        x += v[0], y += v[1], z += v[2];
+// Position gradients of n rows from part0 [s0][n][h0][4] and, for rows that
+// are keys as well, part1 [s1][n][h1][4] (heads and splits in order), and with
+// `slope` the sums over a block's rows of part0's last component,
+// [blocks][h0].  A block has `rows` rows with h0 threads side by side (x).
+__global__ __launch_bounds__(256) void attn_row_kernel(int n, int S, const int* seg, int rows, int h0, int s0,
+                                                       const float* __restrict__ part0, int h1, int s1,
+                                                       const float* __restrict__ part1, float* __restrict__ pos,
+                                                       float* __restrict__ slope) {
+  __shared__ float lds[256][4];
+  const int x = threadIdx.x, y = threadIdx.y, tid = y * blockDim.x + x;
+  float sum = 0.f;
+  const int lo = blockIdx.x * rows, hi = min(n, lo + rows);
+  for (int i0 = lo; i0 < hi; i0 += blockDim.y) {
+    const int i = i0 + y;
+    const bool on = i < hi && in_segments(seg, S, n, i);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (on && x < h0)
+      for (int s = 0; s < s0; ++s) {
+        float p[4];
+        load_f32<float, 4>(part0 + (((size_t)s * n + i) * h0 + x) * 4, p);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] += p[c];
       }
-  };
-  add(h0, s0, p0);
-  if (p1) add(h1, s1, p1);
-  out[3 * (size_t)i] = x, out[3 * (size_t)i + 1] = y, out[3 * (size_t)i + 2] = z;
-}
-
-// slope gradients: sums of a run of rows per block, [blocks][hq]; a thread
-// has one head and every y-th row of the run
-__global__ __launch_bounds__(256) void attn_slope_kernel(int n, int H, int S, const int* seg, int splits, int run,
-                                                         const float* __restrict__ part, float* __restrict__ out) {
-  __shared__ float lds[256];
-  const int h = threadIdx.x, lo = blockIdx.x * run, hi = min(n, lo + run);
-  float t = 0.f;
-  if (h < H)
-    for (int s = 0; s < splits; ++s)
-      for (int i = lo + threadIdx.y; i < hi; i += blockDim.y)
-        if (in_segments(seg, S, n, i)) t += part[(((size_t)s * n + i) * H + h) * 4 + 3];
-  lds[threadIdx.y * blockDim.x + h] = t;
+    sum += v[3];
+    if (!pos) continue;   // the whole launch
+    store_f32<float, 4>(lds[tid], v);
+    __syncthreads();
+    if (on && x < 3) {
+      float t = 0.f;
+      for (int h = 0; h < h0; ++h) t += lds[y * blockDim.x + h][x];
+      for (int s = 0; part1 && s < s1; ++s)
+        for (int h = 0; h < h1; ++h) t += part1[(((size_t)s * n + i) * h1 + h) * 4 + x];
+      pos[3 * (size_t)i + x] = t;
+    }
+    __syncthreads();
+  }
+  if (!slope) return;
+  lds[tid][0] = sum;
   __syncthreads();
-  if (threadIdx.y != 0 || h >= H) return;
-  t = 0.f;
-  for (int y = 0; y < (int)blockDim.y; ++y) t += lds[y * blockDim.x + h];
-  out[(size_t)blockIdx.x * H + h] = t;
+  if (y != 0 || x >= h0) return;
+  sum = 0.f;
+  for (int k = 0; k < (int)blockDim.y; ++k) sum += lds[k * blockDim.x + x][0];
+  slope[(size_t)blockIdx.x * h0 + x] = sum;
 }
 
 // ------------------------------------------------------------------- plans --
@@ -118,6 +123,10 @@ struct PassPlan {
 //  * Few columns over a long walk (single queries): four waves share the walk
 //    (kRows), and blocks in parts of 512 rows, up to two blocks per CU.
 //  * Few columns and rows (molecules): waves go alone (kOne).
+//  * The key pass of wide heads (one wave per SIMD for its registers) takes
+//    kRows also with many columns: with one wave, waiting for the three others
+//    at every tile costs more than the shared loads save (packed batch of 8192
+//    rows, 16 / 4 heads of 128: 215 us against 245 us).
 PassPlan plan_pass(const AttnArgs& a, bool is_bf16, AttnPass pass, int64_t cols, int64_t rows) {
   PassPlan p;
   const int64_t mean = (cols + a.S - 1) / a.S, walk = rows / a.S;
@@ -126,9 +135,11 @@ PassPlan plan_pass(const AttnArgs& a, bool is_bf16, AttnPass pass, int64_t cols,
   };
   p.hb = pass == kAttnFwd && a.slope && attn_two_heads(is_bf16, a.D) && a.hk % 2 == 0 && mean >= 32 ? 2 : 1;
   const int64_t units = (int64_t)a.S * (a.hk / p.hb);
-  if (mean >= 96 || attn_cols_only(is_bf16, a.D)) {
+  if (pass == kAttnKey && is_bf16 && a.D > 64 && mean >= 96 && walk >= 1024) {
+    p.mode = kRows, p.splits = splits((mean + 31) / 32 * units, 4096, 2048);
+  } else if (mean >= 96 || attn_cols_only(is_bf16, a.D)) {
     const int64_t blocks = (mean + 127) / 128 * units;
-    p.mode = kCols, p.splits = mean >= 96 ? splits(blocks, 960, 1024) : splits(blocks, 512, 128);
+    p.mode = kCols, p.splits = mean >= 96 ? splits(blocks, 960, 512 * 2 / p.hb) : splits(blocks, 512, 128);
   } else if (walk >= 256) {
     p.mode = kRows, p.splits = splits((mean + 31) / 32 * units, 512, 512);
   } else {
@@ -137,10 +148,13 @@ PassPlan plan_pass(const AttnArgs& a, bool is_bf16, AttnPass pass, int64_t cols,
   return p;
 }
 
+// rows of a block of attn_row_kernel: a thousand blocks at most
+int rows_per_block(int n) { return std::max(32, (n + 1023) / 1024); }
+
 struct Plan {
   PassPlan fwd, query, key;
   bool exact_delta;   // delta from the scores, not from the rounded out
-  int slope_run, slope_blocks;
+  int slope_blocks;
   AttnPart pf, pd, pq, pk;
   float *row, *col, *slope;
   size_t bytes;
@@ -176,8 +190,7 @@ Plan make_plan(const AttnArgs& a, bool is_bf16, int op, void* ws) {
     if (a.slope) {
       c.row = take(p.query.splits * rq * 4);
       c.col = take(p.key.splits * rk * 4);
-      p.slope_run = std::clamp(a.nq / 1024, 16, 256);
-      p.slope_blocks = (a.nq + p.slope_run - 1) / p.slope_run;
+      p.slope_blocks = (a.nq + rows_per_block(a.nq) - 1) / rows_per_block(a.nq);
       p.slope = take((size_t)p.slope_blocks * a.hq);
     }
     const size_t nq = p.query.splits > 1 ? p.query.splits * rq * a.D : 0;
@@ -260,21 +273,20 @@ void launch_attn_vjp(const AttnArgs& a, bool is_bf16, void* ws, hipStream_t st) 
       sum_splits(is_bf16, a.nk, a.hk * a.D, a.S, a.seg_k, p.key.splits, p.pk.o2, a.gv, st);
     }
   }
-  if (a.g_pos_q && a.nq > 0)
-    hipLaunchKernelGGL(attn_pos_kernel, dim3(blocks_of(a.nq)), dim3(256), 0, st, a.nq, a.S, a.seg_q, a.hq,
-                       p.query.splits, p.pq.row, a.hk, p.key.splits, a.self_pos ? p.pk.col : nullptr, a.g_pos_q);
+  auto rows = [&](int n, const int* seg, int h0, int s0, const float* p0, int h1, int s1, const float* p1, float* pos,
+                  float* slope) {
+    int x = 4;   // three threads at least write a row's position gradient
+    while (x < h0) x <<= 1;
+    const int run = rows_per_block(n);
+    hipLaunchKernelGGL(attn_row_kernel, dim3((n + run - 1) / run), dim3(x, 256 / x), 0, st, n, a.S, seg, run, h0, s0, p0,
+                       h1, s1, p1, pos, slope);
+  };
+  if ((a.g_pos_q || a.g_slope) && a.nq > 0)
+    rows(a.nq, a.seg_q, a.hq, p.query.splits, p.pq.row, a.hk, p.key.splits, a.self_pos ? p.pk.col : nullptr, a.g_pos_q,
+         a.g_slope ? p.slope : nullptr);
   if (a.g_pos_k && a.nk > 0)
-    hipLaunchKernelGGL(attn_pos_kernel, dim3(blocks_of(a.nk)), dim3(256), 0, st, a.nk, a.S, a.seg_k, a.hk,
-                       p.key.splits, p.pk.col, 0, 0, nullptr, a.g_pos_k);
-  if (a.g_slope) {
-    if (a.nq > 0) {
-      int x = 1;
-      while (x < a.hq) x <<= 1;
-      hipLaunchKernelGGL(attn_slope_kernel, dim3(p.slope_blocks), dim3(x, 256 / x), 0, st, a.nq, a.hq, a.S, a.seg_q,
-                         p.query.splits, p.slope_run, p.pq.row, p.slope);
-    }
-    launch_block_sum(p.slope_blocks, a.hq, p.slope, a.g_slope, st);
-  }
+    rows(a.nk, a.seg_k, a.hk, p.key.splits, p.pk.col, 0, 0, nullptr, a.g_pos_k, nullptr);
+  if (a.g_slope) launch_column_sum(p.slope_blocks, a.hq, p.slope, a.g_slope, st);
 }
 
 }  // namespace fc

@@ -46,6 +46,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -74,19 +76,24 @@ __device__ __forceinline__ f32x16 mma_low(const bf16x8 (&a)[3], const bf16x8 (&b
   return mma(a[1], b[0], c);
 }
 
-// x as bfloat16 parts, each rounded to nearest (one: the only rounding)
+// x as bfloat16 parts, each rounded to nearest (one: the only rounding).  Two
+// elements at a time: one conversion for both, and a part is its upper half.
 template <int NP, int N, class V>
 __device__ __forceinline__ void split(const float (&x)[N], V (&p)[NP]) {
-  float r[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) r[i] = x[i];
+  for (int i = 0; i < N; i += 2) {
+    f32x2 r = {x[i], x[i + 1]};
 #pragma unroll
-  for (int k = 0; k < NP; ++k)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      p[k][i] = static_cast<bf16>(r[i]);
-      if (k + 1 < NP) r[i] -= static_cast<float>(p[k][i]);
+    for (int k = 0; k < NP; ++k) {
+      const bf16x2 b = __builtin_convertvector(r, bf16x2);
+      p[k][i] = b[0], p[k][i + 1] = b[1];
+      if (k + 1 < NP) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, b);
+        r[0] -= __builtin_bit_cast(float, u << 16);
+        r[1] -= __builtin_bit_cast(float, u & 0xffff0000u);
+      }
     }
+  }
 }
 
 // Row of register r of the 32x32 result, for the wave's half h.
@@ -245,22 +252,39 @@ __device__ __forceinline__ int opaque(int x) {
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
 __device__ __forceinline__ f32x4 four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 
-// tanh.  fp32 rows: within a few 2^-24 of its value also near 0, where one
-// exponential alone would lose digits.  bfloat16 rows: the exponential alone,
-// a few 2^-24 in absolute terms.
+// The capped score cap tanh(u / cap) / log 2 - ref of a raw product, and the
+// derivative's factor 1 - tanh^2.  bfloat16 rows: with w = 1 / (1 + exp(2 u /
+// cap)) it is c2 - ref - 2 c2 w, and the factor 4 w (1 - w); the error is that
+// of w, a few 2^-24 cap.  fp32 rows: tanh within a few 2^-24 of its value also
+// near 0, where w alone would lose digits.
 template <class T>
-__device__ __forceinline__ float tanh_of(float x) {
-  const float e = __builtin_amdgcn_exp2f(x * (2.f * kLog2e));
-  const float far = fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + e), 1.f);
-  if constexpr (sizeof(T) == 2) return far;
-  const float z = x * x;   // Taylor series; |x| < 0.4 leaves z^7 below 2^-24
-  float p = fmaf(z, 21844.f / 6081075.f, -1382.f / 155925.f);
-  p = fmaf(z, p, 62.f / 2835.f);
-  p = fmaf(z, p, -17.f / 315.f);
-  p = fmaf(z, p, 2.f / 15.f);
-  p = fmaf(z, p, -1.f / 3.f);
-  return z < 0.16f ? fmaf(x * z, p, x) : far;
-}
+struct Cap {
+  float c1, c2;   // scale / cap (bfloat16: times 2 / log 2), cap / log 2
+  __device__ __forceinline__ Cap(float scale, float cap)
+      : c1(scale / cap * (sizeof(T) == 2 ? 2.f * kLog2e : 1.f)), c2(cap * kLog2e) {}
+  __device__ __forceinline__ float score(float u, float ref, float& t) const {
+    if constexpr (sizeof(T) == 2) {
+      t = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u * c1));
+      return fmaf(-2.f * c2, t, c2 - ref);
+    } else {
+      const float x = u * c1, z = x * x;   // Taylor series; |x| < 0.4 leaves z^7 below 2^-24
+      float p = fmaf(z, 21844.f / 6081075.f, -1382.f / 155925.f);
+      p = fmaf(z, p, 62.f / 2835.f);
+      p = fmaf(z, p, -17.f / 315.f);
+      p = fmaf(z, p, 2.f / 15.f);
+      p = fmaf(z, p, -1.f / 3.f);
+      const float far = fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (2.f * kLog2e))), 1.f);
+      t = z < 0.16f ? fmaf(x * z, p, x) : far;
+      return fmaf(c2, t, -ref);
+    }
+  }
+  // ds (1 - tanh^2), for bfloat16 without the 4 (Cap::kRest)
+  static __device__ __forceinline__ float slope(float ds, float t) {
+    if constexpr (sizeof(T) == 2) return ds * fmaf(-t, t, t);
+    return fmaf(-t * t, ds, ds);
+  }
+  static constexpr float kRest = sizeof(T) == 2 ? 4.f : 1.f;
+};
 
 // 1 / r of a squared distance.  Squares carry 1e-35, so that at r = 0 this is
 // a large finite value, which meets differences that are 0 there.
@@ -308,6 +332,8 @@ struct Points {
 };
 
 // ------------------------------------------------- which work a block has --
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 struct Work {
   int tile, head, split;   // column tile in its segment, first key head
@@ -380,9 +406,10 @@ __device__ __forceinline__ Work find_work(const AttnArgs& a, int cols, int hb, i
   } else if (!off) {
     r1 = no;
   }
-  w.q0 = KEYS ? r0 : c0, w.lq = KEYS ? r1 - r0 : c1 - c0;
-  w.k0 = KEYS ? c0 : r0, w.lk = KEYS ? c1 - c0 : r1 - r0;
-  w.pre = a.causal && a.prefix ? clamp(a.prefix[seg], 0, w.lk) : 0;
+  w.q0 = uniform(KEYS ? r0 : c0), w.lq = uniform(KEYS ? r1 - r0 : c1 - c0);
+  w.k0 = uniform(KEYS ? c0 : r0), w.lk = uniform(KEYS ? c1 - c0 : r1 - r0);
+  w.pre = uniform(a.causal && a.prefix ? clamp(a.prefix[seg], 0, w.lk) : 0);
+  w.tile = uniform(w.tile);
   w.any = w.tile >= 0 && (int64_t)w.tile * cols < (int64_t)(KEYS ? w.lk : w.lq) * mul;
   return w;
 }
@@ -412,7 +439,7 @@ struct Waves {
   static constexpr int STAGE = MODE == kCols ? 256 : 64;      // threads that fill one
   static constexpr int STRIDE = MODE == kRows ? 4 : 1;        // tiles from one to the next of a wave
   static __device__ __forceinline__ int stage_thread() { return MODE == kCols ? threadIdx.x : threadIdx.x % 64; }
-  static __device__ __forceinline__ int region() { return MODE == kRows ? threadIdx.x / 64 : 0; }
+  static __device__ __forceinline__ int region() { return MODE == kRows ? uniform(threadIdx.x / 64) : 0; }
   // between the writes and the reads of a tile
   static __device__ __forceinline__ void sync() {
     if constexpr (MODE == kCols)
@@ -490,7 +517,8 @@ template <class T, int DP, int HB, int MODE, bool BIAS>
 constexpr int waves_per_simd(int frags, int accs, int live, int rows) {
   using TL = Tile<T, DP, HB>;
   const int regs = frags * HB * TL::STEPS * TL::NP * 4 + accs * HB * TL::DB * 16 + live * 16 +
-                   2 * 4 * ((rows * TL::CPR + Waves<MODE>::STAGE - 1) / Waves<MODE>::STAGE) + (BIAS ? 100 : 60);
+                   2 * 4 * ((rows * TL::CPR + Waves<MODE>::STAGE - 1) / Waves<MODE>::STAGE) + (BIAS ? 100 : 60) +
+                   (accs == 2 && TL::NP == 3 ? 40 : 0);
   return regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
 }
 
@@ -520,7 +548,7 @@ void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
   __shared__ __align__(16) float lpos[BIAS ? WV::REGIONS * 3 * ROWS : 4];
   const Work w = find_work<false>(a, WV::COLS, HB, tiles, part.splits);
   if (!w.any) return;   // the whole block
-  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32, st = WV::stage_thread();
+  const int lane = threadIdx.x % 64, wv = uniform(threadIdx.x / 64), h = lane / 32, st = WV::stage_thread();
   const int col = w.tile * WV::COLS + (MODE == kCols ? wv * 32 : 0) + lane % 32;
   const int i = col / a.G, head = w.head * a.G + col % a.G;   // + hb G for the other heads
   const bool live = i < w.lq;
@@ -570,7 +598,8 @@ void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
   }
   float px = 0.f, py = 0.f, pz = 0.f;
   if (BIAS && live) px = a.pos_q[3 * qrow], py = a.pos_q[3 * qrow + 1], pz = a.pos_q[3 * qrow + 2];
-  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+  const float c1 = a.scale * kLog2e;
+  const Cap<T> cap(a.scale, a.cap);
 
   bool first = true;
   auto tile = [&](bool edge, int j0) {
@@ -602,9 +631,9 @@ void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
       for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          float x;
+          float x, t;
           if constexpr (CAP)
-            x = fmaf(c2, tanh_of<T>(s[hb][n][r] * c1), -m[hb]);
+            x = cap.score(s[hb][n][r], m[hb], t);
           else
             x = fmaf(s[hb][n][r], c1, -m[hb]);
           if constexpr (BIAS) x = fmaf(-slope[hb], dist[n][r], x);
@@ -634,7 +663,9 @@ void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
     if (__any(raise)) {
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb) {
-        const float up = mx[hb] == -kInf ? 0.f : first ? mx[hb] : fmaxf(mx[hb], 0.f), f = __builtin_amdgcn_exp2f(-up);
+        // whole numbers, so that m has no rest (c2 - m does not round)
+        const float up = mx[hb] == -kInf ? 0.f : rintf(first ? mx[hb] : fmaxf(mx[hb], 0.f));
+        const float f = __builtin_amdgcn_exp2f(-up);
         m[hb] += up;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -742,7 +773,7 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
   const int splits = DELTA ? part.dsplits : part.splits;
   const Work w = find_work<false>(a, WV::COLS, 1, tiles, splits);
   if (!w.any) return;
-  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32, st = WV::stage_thread();
+  const int lane = threadIdx.x % 64, wv = uniform(threadIdx.x / 64), h = lane / 32, st = WV::stage_thread();
   const int col = w.tile * WV::COLS + (MODE == kCols ? wv * 32 : 0) + lane % 32;
   const int i = col / a.G, head = w.head * a.G + col % a.G;
   const bool live = i < w.lq, lead = live && h == 0 && (MODE != kRows || wv == 0);
@@ -806,7 +837,8 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
   for (int b = 0; b < TL::DB; ++b) dq[0][b] = f32x16{};
   float px = 0.f, py = 0.f, pz = 0.f;
   if (BIAS && live) px = a.pos_q[3 * qrow], py = a.pos_q[3 * qrow + 1], pz = a.pos_q[3 * qrow + 2];
-  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+  const float c1 = a.scale * kLog2e;
+  const Cap<T> cap(a.scale, a.cap);
   float v[4] = {0.f, 0.f, 0.f, 0.f}, dsum[1] = {0.f};   // position and slope gradients; delta
 
   auto tile = [&](bool edge, int j0) {
@@ -828,9 +860,8 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
         const int r = r4 * 4 + e;
         float th = 0.f, x, inv, d;
         if constexpr (CAP) {
-          th = tanh_of<T>(s[r] * c1);
-          x = fmaf(c2, th, -norm.ref);
-          if (edge && j0 + acc_row(r, h) >= vis) x = -kInf;
+          x = cap.score(s[r], norm.ref, th);
+          if ((BIAS || DELTA) && edge && j0 + acc_row(r, h) >= vis) x = -kInf;
         } else {
           x = fmaf(s[r], c1, -norm.ref);
         }
@@ -848,10 +879,16 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
             gs = fmaf(ds, d, gs);
             pt.add(e, ds * inv, gp);   // the slope is the column's own: at the end
           }
-          if constexpr (CAP) ds = fmaf(-th * th, ds, ds);
+          if constexpr (CAP) ds = Cap<T>::slope(ds, th);
           s[r] = ds;
         }
       }
+    }
+    if (CAP && !BIAS && !DELTA && edge) {
+      const int last = opaque(vis) - j0;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (acc_row(r, h) >= last) s[r] = 0.f;
     }
     if constexpr (DELTA) dsum[0] += gd;
     if constexpr (BIAS && !DELTA) v[0] += gp[0], v[1] += gp[1], v[2] += gp[2], v[3] += gs;
@@ -886,7 +923,7 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
 #pragma unroll
   for (int b = 0; b < TL::DB; ++b)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dq[0][b][r] *= norm.factor;
+    for (int r = 0; r < 16; ++r) dq[0][b][r] *= norm.factor * (CAP ? Cap<T>::kRest : 1.f);
   auto put = [&](size_t row, int d, const float* x) {
     const float y[4] = {x[0] * a.scale, x[1] * a.scale, x[2] * a.scale, x[3] * a.scale};
     if (part.splits == 1)
@@ -927,7 +964,7 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
   __shared__ __align__(16) QueryTile<ROWS, BIAS> lrow[WV::REGIONS];
   const Work w = find_work<true>(a, WV::COLS, 1, tiles, part.splits);
   if (!w.any) return;
-  const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, h = lane / 32, st = WV::stage_thread();
+  const int lane = threadIdx.x % 64, wv = uniform(threadIdx.x / 64), h = lane / 32, st = WV::stage_thread();
   const int j = w.tile * WV::COLS + (MODE == kCols ? wv * 32 : 0) + lane % 32;
   const bool live = j < w.lk;
   const size_t krow = w.k0 + j, nrows = (size_t)a.nq * a.hq;
@@ -1003,7 +1040,8 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
   for (int b = 0; b < TL::DB; ++b) dk[0][b] = f32x16{}, dv[0][b] = f32x16{};
   float px = 0.f, py = 0.f, pz = 0.f;
   if (BIAS && live) px = a.pos_k[3 * krow], py = a.pos_k[3 * krow + 1], pz = a.pos_k[3 * krow + 2];
-  const float c1 = CAP ? a.scale / a.cap : a.scale * kLog2e, c2 = a.cap * kLog2e;
+  const float c1 = a.scale * kLog2e;
+  const Cap<T> cap(a.scale, a.cap);
   float gp[3] = {0.f, 0.f, 0.f};
 
   auto tile = [&](bool edge) {
@@ -1025,7 +1063,7 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
       const int rr = r4 * 8 + h * 4, pp = BIAS ? rr : 0;
       const f32x4 ref = four(lr.ref + rr), factor = four(lr.factor + rr), delta = four(lr.delta + rr);
       i32x4 vis;
-      if constexpr (CAP) vis = *reinterpret_cast<const i32x4*>(lr.vis + rr);
+      if constexpr (CAP && BIAS) vis = *reinterpret_cast<const i32x4*>(lr.vis + rr);
       const Points pt(px, py, pz, lr.pos[0] + pp, lr.pos[BIAS ? 1 : 0] + pp, lr.pos[BIAS ? 2 : 0] + pp);
       f32x4 sl;
       if constexpr (BIAS) sl = four(lr.slope + rr);
@@ -1034,9 +1072,8 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
         const int r = r4 * 4 + e;
         float th = 0.f, x, inv;
         if constexpr (CAP) {
-          th = tanh_of<T>(s[r] * c1);
-          x = fmaf(c2, th, -ref[e]);
-          if (edge && j >= vis[e]) x = -kInf;
+          x = cap.score(s[r], ref[e], th);
+          if (BIAS && edge && j >= vis[e]) x = -kInf;
         } else {
           x = fmaf(s[r], c1, -ref[e]);
         }
@@ -1047,9 +1084,19 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
         const float p = __builtin_amdgcn_exp2f(x) * factor[e];
         float ds = p * (dp[r] - delta[e]);
         if constexpr (BIAS) pt.add(e, ds * inv * sl[e], gt);
-        if constexpr (CAP) ds = fmaf(-th * th, ds, ds);
+        if constexpr (CAP) ds = Cap<T>::slope(ds, th);
         s[r] = p;
         dp[r] = ds;
+      }
+    }
+    if (CAP && !BIAS && edge) {
+      const int jj = opaque(j);
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const i32x4 vis = *reinterpret_cast<const i32x4*>(lr.vis + r4 * 8 + h * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (jj >= vis[e]) s[r4 * 4 + e] = dp[r4 * 4 + e] = 0.f;
       }
     }
     if constexpr (BIAS) gp[0] += gt[0], gp[1] += gt[1], gp[2] += gt[2];
@@ -1106,7 +1153,7 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
       });
     }
   };
-  write(dk, a.gk, part.o, a.scale);
+  write(dk, a.gk, part.o, a.scale * (CAP ? Cap<T>::kRest : 1.f));
   write(dv, a.gv, part.o2, 1.f);
 }
 

@@ -23,7 +23,7 @@
 namespace fc {
 namespace {
 
-constexpr int kSortThreads = 256, kSortRounds = 8, kSortItems = kSortThreads * kSortRounds;
+constexpr int kSortThreads = 256, kSortRounds = 4, kSortItems = kSortThreads * kSortRounds;
 constexpr int kSortWaves = kSortThreads / 64;
 
 template <class T, int V>
@@ -118,14 +118,19 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(int N, int R
   const int t = threadIdx.x, lane = t % 64, w = t / 64, ndig = 1 << bits;
 #pragma unroll
   for (int i = 0; i < kSortWaves; ++i) cnt[i][t] = 0;
-  __syncthreads();
   const int base = blockIdx.x * kSortItems + w * (kSortItems / kSortWaves);
   int key[kSortRounds], rank[kSortRounds];
 #pragma unroll
   for (int i = 0; i < kSortRounds; ++i) {
     const int n = base + i * 64 + lane;
-    const bool in = n < N;
-    key[i] = in ? (first_pass ? key_of(keys[n], R) : keys[n]) : 0;
+    key[i] = n < N ? (first_pass ? key_of(keys[n], R) : keys[n]) : 0;
+  }
+  const int digits = t < ndig ? total[t] : 0;
+  const int before = t < ndig ? hist[(size_t)t * gridDim.x + blockIdx.x] : 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    const bool in = base + i * 64 + lane < N;
     const int d = (key[i] >> shift) & (ndig - 1);
     unsigned long long peers = __ballot(in);
     for (int b = 0; b < bits; ++b) {
@@ -143,7 +148,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(int N, int R
   }
   __syncthreads();
   {  // digit t: first position = digits before + blocks before + waves before
-    const int v = t < ndig ? total[t] : 0;
+    const int v = digits;
     int s = v;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -156,7 +161,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(int N, int R
 #pragma unroll
     for (int i = 0; i < kSortWaves; ++i)
       if (i < w) run += sums[i];
-    if (t < ndig) run += hist[(size_t)t * gridDim.x + blockIdx.x];
+    run += before;
 #pragma unroll
     for (int i = 0; i < kSortWaves; ++i) {
       const int c = cnt[i][t];
@@ -218,16 +223,29 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(int N, int R, int C, int
     for (int i = 0; i < V; ++i) acc[i] *= f;
     store_f32<float, V>(dst + c, acc);
   };
-  constexpr int U = 8;   // rows in flight
+  // U rows in flight; their keys and places are read a batch ahead, by one
+  // lane each where a group has that many
+  constexpr int U = 16;
+  const int gl = threadIdx.x % group, g0 = threadIdx.x % 64 - gl;
+  const bool shared = group >= U;
+  int kn = 0, on = 0;
+  auto ahead = [&](int p) {
+    const int q = min(p + gl % U, p1 - 1);
+    kn = key[q];
+    on = ord[q];
+  };
+  if (shared) ahead(p0);
   for (int p = p0; p < p1; p += U) {
     int k[U];
-    float x[U][V];
+    Pack<T, V> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int q = min(p + u, p1 - 1);
-      k[u] = key[q];
-      if (live && k[u] < R) load_f32<T, V>(g + (size_t)ord[q] * C + c, x[u]);
+      k[u] = shared ? __shfl(kn, g0 + u) : key[q];
+      const int o = shared ? __shfl(on, g0 + u) : ord[q];
+      if (live && k[u] < R) x[u] = *reinterpret_cast<const Pack<T, V>*>(g + (size_t)o * C + c);
     }
+    if (shared && p + U < p1) ahead(p + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (p + u >= p1) break;
@@ -240,70 +258,81 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(int N, int R, int C, int
       }
       if (cur >= R) return;   // padding is sorted last
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += x[u][i];
+      for (int i = 0; i < V; ++i) acc[i] += static_cast<float>(x[u].e[i]);
     }
   }
   flush(p1);
 }
 
-// Rows whose run is cut by chunk edges, and rows without a token.  Each wave
-// takes a row; rows of more than kLong pieces are left to the whole block,
-// whose waves take pieces in turn and add up in wave order.
+// Rows whose run is cut by chunk edges, and rows without a token.  A wave
+// takes RW rows, whose bounds it reads at once.  The rows of a block lie a
+// grid apart, so that neighbouring frequent rows (tables are often ordered by
+// frequency) fall to different blocks.  Rows of more than kLong pieces
+// are left to the whole block, whose waves take pieces in turn and add up in
+// wave order.
 constexpr int kLong = 16;
-template <int W, int V>
-__global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int chunk, float scale, int rows,
+template <int W, int RW, int V>
+__global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int chunk, float scale,
                                                             const int* __restrict__ first,
                                                             const int* __restrict__ last,
                                                             const float* __restrict__ part, float* __restrict__ grad) {
+  // rows of the block: RW per wave, or one for all of a block of RW = 1
+  constexpr int ROWS = RW == 1 ? 1 : W * RW;
   __shared__ float sum[W][64 * V];
+  __shared__ int bound[2][ROWS];
   const int w = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const int r0 = blockIdx.x * rows, r1 = min(R, r0 + rows);
-  // piece j of the run of chunks a..b: slot 1 of a unless the run begins there
+  auto row = [&](int i) { return (int)(blockIdx.x + i * gridDim.x); };
+  const int rows = (R - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // at most ROWS
+  for (int i = threadIdx.x; i < rows; i += W * 64) bound[0][i] = first[row(i)], bound[1][i] = last[row(i)];
+  __syncthreads();
+  // piece of the run of chunks a..b: slot 1 of a unless the run begins there
   auto slot = [&](int f, int ch) { return part + ((size_t)ch * 2 + (ch * chunk < f ? 1 : 0)) * C; };
-  for (int r = r0 + w; r < r1; r += W) {
-    const int f = first[r], l = last[r];
-    const int a = f / chunk, b = (l - 1) / chunk;
-    if (l > f && (a == b || b - a >= kLong)) continue;
+  bool any_long = false;
+  for (int i = 0; i < rows; ++i) {
+    const int f = bound[0][i], l = bound[1][i], a = f / chunk, b = (l - 1) / chunk;
+    const bool is_long = l > f && b - a >= kLong;
+    any_long |= is_long;
+    if (i / (RW == 1 ? W : RW) != w || is_long || (l > f && a == b)) continue;
     for (int c = lane * V; c < C; c += 64 * V) {
       float acc[V] = {};
       for (int ch = a; l > f && ch <= b; ++ch) {
         float x[V];
         load_f32<float, V>(slot(f, ch) + c, x);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += x[i];
+        for (int e = 0; e < V; ++e) acc[e] += x[e];
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] *= scale;
-      store_f32<float, V>(grad + (size_t)r * C + c, acc);
+      for (int e = 0; e < V; ++e) acc[e] *= scale;
+      store_f32<float, V>(grad + (size_t)row(i) * C + c, acc);
     }
   }
-  for (int r = r0; r < r1; ++r) {
-    const int f = first[r], l = last[r];
-    const int a = f / chunk, b = (l - 1) / chunk;
-    if (l <= f || b - a < kLong) continue;   // the same for the whole block
+  if (!any_long) return;   // the same for the whole block
+  for (int i = 0; i < rows; ++i) {
+    const int f = bound[0][i], l = bound[1][i], a = f / chunk, b = (l - 1) / chunk;
+    if (l <= f || b - a < kLong) continue;
     for (int c0 = 0; c0 < C; c0 += 64 * V) {
       const int c = c0 + lane * V;
       float acc[V] = {};
       if (c < C) {
-#pragma unroll 4
+#pragma unroll 8
         for (int ch = a + w; ch <= b; ch += W) {
           float x[V];
           load_f32<float, V>(slot(f, ch) + c, x);
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] += x[i];
+          for (int e = 0; e < V; ++e) acc[e] += x[e];
         }
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[w][lane * V + i] = acc[i];
+      for (int e = 0; e < V; ++e) sum[w][lane * V + e] = acc[e];
       __syncthreads();
       if (w == 0 && c < C) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int e = 0; e < V; ++e) {
           float t = 0.f;
-          for (int j = 0; j < W; ++j) t += sum[j][lane * V + i];
-          acc[i] = t * scale;
+          for (int j = 0; j < W; ++j) t += sum[j][lane * V + e];
+          acc[e] = t * scale;
         }
-        store_f32<float, V>(grad + (size_t)r * C + c, acc);
+        store_f32<float, V>(grad + (size_t)row(i) * C + c, acc);
       }
       __syncthreads();
     }
@@ -339,10 +368,11 @@ void sum_t(const EmbedPlan& p, float scale, const int* key, const int* ord, cons
                      p.first, p.last);
 }
 
-template <int W, int V>
-void join_t(const EmbedPlan& p, float scale, float* grad, int rows, hipStream_t st) {
-  hipLaunchKernelGGL((embed_join_kernel<W, V>), dim3((p.R + rows - 1) / rows), dim3(W * 64), 0, st, p.R, p.C, p.chunk,
-                     scale, rows, p.first, p.last, p.part, grad);
+template <int W, int RW, int V>
+void join_t(const EmbedPlan& p, float scale, float* grad, hipStream_t st) {
+  constexpr int rows = RW == 1 ? 1 : W * RW;
+  hipLaunchKernelGGL((embed_join_kernel<W, RW, V>), dim3((p.R + rows - 1) / rows), dim3(W * 64), 0, st, p.R, p.C,
+                     p.chunk, scale, p.first, p.last, p.part, grad);
 }
 
 }  // namespace
@@ -412,12 +442,11 @@ void launch_embed_vjp(const EmbedPlan& p, bool is_bf16, float scale, const int* 
     p.vec > 1 ? sum_t<bf16, 8>(p, scale, key, ord, g, grad, st) : sum_t<bf16, 1>(p, scale, key, ord, g, grad, st);
   else
     p.vec > 1 ? sum_t<float, 4>(p, scale, key, ord, g, grad, st) : sum_t<float, 1>(p, scale, key, ord, g, grad, st);
-  // few rows: a block of 16 waves for each; many: four waves for several rows
-  const int rows = std::clamp(p.R / 4096, 1, 16);
-  if (rows == 1)
-    p.vec > 1 ? join_t<16, 4>(p, scale, grad, 1, st) : join_t<16, 1>(p, scale, grad, 1, st);
+  // few rows: a block of 16 waves for each; many: each wave a run of rows
+  if (p.R <= 4096)
+    p.vec > 1 ? join_t<16, 1, 4>(p, scale, grad, st) : join_t<16, 1, 1>(p, scale, grad, st);
   else
-    p.vec > 1 ? join_t<4, 4>(p, scale, grad, rows, st) : join_t<4, 1>(p, scale, grad, rows, st);
+    p.vec > 1 ? join_t<4, 8, 4>(p, scale, grad, st) : join_t<4, 8, 1>(p, scale, grad, st);
 }
 
 }  // namespace fc

@@ -254,9 +254,10 @@ __global__ __launch_bounds__(kWaves * 64) void qk_rope_vjp_kernel(QkRopeArgs A, 
   }
 }
 
-// Pairs per lane: 16-byte pieces where the halves and the rows allow them.
-int pairs_per_lane(const QkRopeArgs& a) {
-  const int e = a.bf16 ? 2 : 4, full = 16 / e;
+// Pairs per lane: 16-byte pieces where the halves and the rows allow them, in
+// the VJP four pairs at most.
+int pairs_per_lane(const QkRopeArgs& a, bool vjp) {
+  const int e = a.bf16 ? 2 : 4, full = vjp ? 4 : 16 / e;
   auto fits = [&](int v) {
     auto on = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % (v * e) == 0; };
     auto on4 = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % (v * 4) == 0; };
@@ -313,7 +314,7 @@ int qk_rope_vjp_blocks(const QkRopeArgs& a) {
 }
 
 void launch_qk_rope_fwd(const QkRopeArgs& a, hipStream_t st) {
-  const int vec = pairs_per_lane(a);
+  const int vec = pairs_per_lane(a, false);
   const Shape s = shape_of(a, vec);
   dispatch(a, vec, [&](auto t, auto v, auto inter) {
     hipLaunchKernelGGL((qk_rope_fwd_kernel<decltype(t), decltype(v)::value, decltype(inter)::value>),
@@ -322,15 +323,15 @@ void launch_qk_rope_fwd(const QkRopeArgs& a, hipStream_t st) {
 }
 
 void launch_qk_rope_vjp(const QkRopeArgs& a, float* gamma_q_grad, float* gamma_k_grad, hipStream_t st) {
-  const int vec = pairs_per_lane(a);
+  const int vec = pairs_per_lane(a, true);
   const Shape s = shape_of(a, vec);
   const int blocks = std::min((s.waves + kWaves - 1) / kWaves, qk_rope_vjp_blocks(a));
   dispatch(a, vec, [&](auto t, auto v, auto inter) {
     hipLaunchKernelGGL((qk_rope_vjp_kernel<decltype(t), decltype(v)::value, decltype(inter)::value>), dim3(blocks),
                        dim3(kWaves * 64), 0, st, a, s.group, s.share);
   });
-  if (gamma_q_grad) launch_block_sum(blocks, a.D, a.part, gamma_q_grad, st);
-  if (gamma_k_grad) launch_block_sum(blocks, a.D, a.part + (size_t)blocks * a.D, gamma_k_grad, st);
+  if (gamma_q_grad) launch_column_sum(blocks, a.D, a.part, gamma_q_grad, st);
+  if (gamma_k_grad) launch_column_sum(blocks, a.D, a.part + (size_t)blocks * a.D, gamma_k_grad, st);
 }
 
 }  // namespace fc

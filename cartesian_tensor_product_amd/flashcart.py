@@ -505,81 +505,90 @@ def _bad(msg: str):
     return FlashCartError(FC_ERR_INVALID_ARGUMENT, msg)
 
 
-class _Args:
-    """Marshals the tensors of one call: all on one GPU, of the given dtype
-    and shape, contiguous but for the row stride where one is allowed."""
+def _place(t, name: str) -> int:
+    """Index of the GPU that a call runs on: that of its leading tensor (-1
+    without one; the library then refuses the call)."""
+    import torch
+    if t is None:
+        return -1
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: tensor must live on the GPU")
+    return dev
 
-    def __init__(self, dtype: int, stream, workspace=None):
-        import torch
-        self.torch = torch
-        self.elem = torch.bfloat16 if dtype == FC_BF16 else torch.float32
-        self.device = None
-        self.stream = stream
-        self.ws = self(workspace, torch.uint8, None, "workspace")
-        self.ws_bytes = 0 if workspace is None else workspace.numel()
 
-    def __call__(self, t, dtype, shape, name):
-        if t is None:
-            return None
-        if not isinstance(t, self.torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: tensor must live on the GPU")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name}: tensor on {t.device}, the others on {self.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-        if shape is not None and t.shape != shape:
-            raise _bad(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: tensor must be contiguous")
-        return t.data_ptr()
+def _refuse(t, dtype, shape, dev, name):
+    _place(t, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor on cuda:{t.get_device()}, the others on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise _bad(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: tensor must be contiguous")
 
-    def f32(self, t, shape, name):
-        return self(t, self.torch.float32, shape, name)
 
-    def i32(self, t, shape, name):
-        return self(t, self.torch.int32, shape, name)
+def _arr(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of this dtype and shape on GPU dev (None
+    passes).  Few attribute reads: small calls are bound by the host."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == dev and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, shape, dev, name)
 
-    def data(self, t, shape, name):
-        return self(t, self.elem, shape, name)
 
-    def rows(self, t, shape, name):
-        """(pointer, row stride in elements; 0 for packed rows)"""
-        if t is None or not isinstance(t, self.torch.Tensor) or t.is_contiguous():
-            return self(t, self.elem, shape, name), 0
-        if t.shape != shape:
-            raise _bad(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if (shape[2] > 1 and t.stride(2) != 1) or (shape[1] > 1 and t.stride(1) != shape[2]):
-            raise ValueError(f"{name}: the heads of a row must be contiguous")
-        stride = t.stride(0)
-        if stride < shape[1] * shape[2]:
-            raise _bad(f"{name}: rows overlap (stride {stride})")
-        self(t[:1], self.elem, None, name)   # device and dtype
-        return t.data_ptr(), stride
+def _rows(t, dtype, shape, dev, name):
+    """(pointer, row stride in elements; 0 for packed rows) of [rows][heads][dim]."""
+    if t is None or not hasattr(t, "is_contiguous") or t.is_contiguous():
+        return _arr(t, dtype, shape, dev, name), 0
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, dtype, shape, dev, name)
+    if (shape[2] > 1 and t.stride(2) != 1) or (shape[1] > 1 and t.stride(1) != shape[2]):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    stride = t.stride(0)
+    if stride < shape[1] * shape[2]:
+        raise _bad(f"{name}: rows overlap (stride {stride})")
+    return t.data_ptr(), stride
 
-    def call(self, f, *args):
-        torch = self.torch
-        if self.device is None:
-            return _check(f(*args, self._stream_of(None)))
-        if self.device.index == torch.cuda.current_device():
-            return _check(f(*args, self._stream_of(self.device)))
-        with torch.cuda.device(self.device):
-            _check(f(*args, self._stream_of(self.device)))
 
-    def _stream_of(self, device):
-        s = self.stream
-        if s is None:
-            s = self.torch.cuda.current_stream(device)
-        return getattr(s, "cuda_stream", s)
+def _elem(dtype: int):
+    import torch
+    return torch.bfloat16 if dtype == FC_BF16 else torch.float32
+
+
+def _run(f, dev: int, stream, *args):
+    """f(*args, stream) with GPU dev current; the stream defaults to its
+    current one."""
+    import torch
+    if dev < 0:
+        return _check(f(*args, None))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream without the object
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
+    if dev == torch.cuda.current_device():
+        _check(f(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, stream))
+
+
+def _ws(workspace, dev):
+    import torch
+    return (None, 0) if workspace is None else (_arr(workspace, torch.uint8, None, dev, "workspace"), workspace.numel())
 
 
 def fc_embed_fwd(d: EmbedDesc, table, ids, out, stream=None):
-    a = _Args(d.dtype, stream)
-    a.call(lib().fc_embed_fwd, d, a.data(table, (d.n_rows, d.channels), "table"), a.i32(ids, (d.n_tokens,), "ids"),
-           a.data(out, (d.n_tokens, d.channels), "out"))
+    import torch
+    dev, elem, n, c = _place(table, "table"), _elem(d.dtype), d.n_tokens, d.channels
+    _run(lib().fc_embed_fwd, dev, stream, d, _arr(table, elem, (d.n_rows, c), dev, "table"),
+         _arr(ids, torch.int32, (n,), dev, "ids"), _arr(out, elem, (n, c), dev, "out"))
 
 
 def fc_embed_workspace_bytes(d: EmbedDesc) -> int:
@@ -587,28 +596,30 @@ def fc_embed_workspace_bytes(d: EmbedDesc) -> int:
 
 
 def fc_embed_vjp(d: EmbedDesc, ids, g_out, table_grad, workspace, stream=None):
-    a = _Args(d.dtype, stream, workspace)
-    a.call(lib().fc_embed_vjp, d, a.i32(ids, (d.n_tokens,), "ids"),
-           a.data(g_out, (d.n_tokens, d.channels), "g_out"),
-           a.f32(table_grad, (d.n_rows, d.channels), "table_grad"), a.ws, a.ws_bytes)
+    import torch
+    dev, n, c = _place(table_grad, "table_grad"), d.n_tokens, d.channels
+    _run(lib().fc_embed_vjp, dev, stream, d, _arr(ids, torch.int32, (n,), dev, "ids"),
+         _arr(g_out, _elem(d.dtype), (n, c), dev, "g_out"),
+         _arr(table_grad, torch.float32, (d.n_rows, c), dev, "table_grad"), *_ws(workspace, dev))
 
 
-def _qk_inputs(a: _Args, d: QkRopeDesc, q, k, gamma_q, gamma_k, pos, freq):
-    n, dim = d.n_nodes, d.head_dim
-    pq, sq = a.rows(q, (n, d.heads_q, dim), "q")
-    pk, sk = a.rows(k, (n, d.heads_k, dim), "k")
+def _qk_inputs(d: QkRopeDesc, elem, dev, q, k, gamma_q, gamma_k, pos, freq):
+    import torch
+    n, dim, f32 = d.n_nodes, d.head_dim, torch.float32
+    pq, sq = _rows(q, elem, (n, d.heads_q, dim), dev, "q")
+    pk, sk = _rows(k, elem, (n, d.heads_k, dim), dev, "k")
     if sq or sk:
         d = QkRopeDesc.from_buffer_copy(d)
         d.q_stride, d.k_stride = sq, sk
-    return (d, pq, pk, a.f32(gamma_q, (dim,), "gamma_q"), a.f32(gamma_k, (dim,), "gamma_k"),
-            a.f32(pos, (n, 3), "pos"), a.f32(freq, (d.n_freq, 3), "freq"))
+    return (d, pq, pk, _arr(gamma_q, f32, (dim,), dev, "gamma_q"), _arr(gamma_k, f32, (dim,), dev, "gamma_k"),
+            _arr(pos, f32, (n, 3), dev, "pos"), _arr(freq, f32, (d.n_freq, 3), dev, "freq"))
 
 
 def fc_qk_norm_rope_fwd(d: QkRopeDesc, q, k, gamma_q, gamma_k, pos, freq, q_out, k_out, stream=None):
-    a = _Args(d.dtype, stream)
+    dev, elem = _place(q, "q"), _elem(d.dtype)
     n, dim = d.n_nodes, d.head_dim
-    a.call(lib().fc_qk_norm_rope_fwd, *_qk_inputs(a, d, q, k, gamma_q, gamma_k, pos, freq),
-           a.data(q_out, (n, d.heads_q, dim), "q_out"), a.data(k_out, (n, d.heads_k, dim), "k_out"))
+    _run(lib().fc_qk_norm_rope_fwd, dev, stream, *_qk_inputs(d, elem, dev, q, k, gamma_q, gamma_k, pos, freq),
+         _arr(q_out, elem, (n, d.heads_q, dim), dev, "q_out"), _arr(k_out, elem, (n, d.heads_k, dim), dev, "k_out"))
 
 
 def fc_qk_norm_rope_workspace_bytes(d: QkRopeDesc) -> int:
@@ -617,13 +628,15 @@ def fc_qk_norm_rope_workspace_bytes(d: QkRopeDesc) -> int:
 
 def fc_qk_norm_rope_vjp(d: QkRopeDesc, q, k, gamma_q, gamma_k, pos, freq, g_q, g_k, q_grad, k_grad, gamma_q_grad,
                         gamma_k_grad, pos_grad, workspace, stream=None):
-    a = _Args(d.dtype, stream, workspace)
+    import torch
+    dev, elem, f32 = _place(q, "q"), _elem(d.dtype), torch.float32
     n, dim = d.n_nodes, d.head_dim
     sq, sk = (n, d.heads_q, dim), (n, d.heads_k, dim)
-    a.call(lib().fc_qk_norm_rope_vjp, *_qk_inputs(a, d, q, k, gamma_q, gamma_k, pos, freq),
-           a.data(g_q, sq, "g_q"), a.data(g_k, sk, "g_k"), a.data(q_grad, sq, "q_grad"), a.data(k_grad, sk, "k_grad"),
-           a.f32(gamma_q_grad, (dim,), "gamma_q_grad"), a.f32(gamma_k_grad, (dim,), "gamma_k_grad"),
-           a.f32(pos_grad, (n, 3), "pos_grad"), a.ws, a.ws_bytes)
+    _run(lib().fc_qk_norm_rope_vjp, dev, stream, *_qk_inputs(d, elem, dev, q, k, gamma_q, gamma_k, pos, freq),
+         _arr(g_q, elem, sq, dev, "g_q"), _arr(g_k, elem, sk, dev, "g_k"), _arr(q_grad, elem, sq, dev, "q_grad"),
+         _arr(k_grad, elem, sk, dev, "k_grad"), _arr(gamma_q_grad, f32, (dim,), dev, "gamma_q_grad"),
+         _arr(gamma_k_grad, f32, (dim,), dev, "gamma_k_grad"), _arr(pos_grad, f32, (n, 3), dev, "pos_grad"),
+         *_ws(workspace, dev))
 
 
 def fc_segments_validate(n_segments: int, n_rows: int, offsets) -> None:
@@ -670,22 +683,26 @@ class Segments:
         self.struct = SegmentPtrs(ptr(self.q), ptr(self.k), ptr(self.prefix))
 
 
-def _attn_inputs(a: _Args, d: AttnDesc, seg, q, k, v, slope, pos_q, pos_k):
+def _attn_inputs(d: AttnDesc, elem, dev, seg, q, k, v, slope, pos_q, pos_k):
+    import torch
+    f32 = torch.float32
+    nq, nk, hq, hk, dim = d.n_query, d.n_key, d.heads_q, d.heads_k, d.head_dim
     if seg is not None:
         if seg.n_segments != d.n_segments:
             raise _bad(f"{seg.n_segments} segments, the descriptor has {d.n_segments}")
-        if seg.n_query > d.n_query or seg.n_key > d.n_key:
-            raise _bad(f"segments end at rows {seg.n_query}, {seg.n_key}, beyond the descriptor's {d.n_query}, {d.n_key}")
-        a.i32(seg.q, None, "segments")
-    kv = (d.n_key, d.heads_k, d.head_dim)
-    pq, sq = a.rows(q, (d.n_query, d.heads_q, d.head_dim), "q")
-    pk, sk = a.rows(k, kv, "k")
-    pv, sv = a.rows(v, kv, "v")
+        if seg.n_query > nq or seg.n_key > nk:
+            raise _bad(f"segments end at rows {seg.n_query}, {seg.n_key}, beyond the descriptor's {nq}, {nk}")
+        if seg.q.get_device() != dev:
+            raise ValueError(f"segments: offsets on another device than cuda:{dev}")
+        seg = seg.struct
+    pq, sq = _rows(q, elem, (nq, hq, dim), dev, "q")
+    pk, sk = _rows(k, elem, (nk, hk, dim), dev, "k")
+    pv, sv = _rows(v, elem, (nk, hk, dim), dev, "v")
     if sq or sk or sv:
         d = AttnDesc.from_buffer_copy(d)
         d.q_stride, d.k_stride, d.v_stride = sq, sk, sv
-    return (d, None if seg is None else seg.struct, pq, pk, pv, a.f32(slope, (d.heads_q,), "slope"),
-            a.f32(pos_q, (d.n_query, 3), "pos_q"), a.f32(pos_k, (d.n_key, 3), "pos_k"))
+    return (d, seg, pq, pk, pv, _arr(slope, f32, (hq,), dev, "slope"), _arr(pos_q, f32, (nq, 3), dev, "pos_q"),
+            _arr(pos_k, f32, (nk, 3), dev, "pos_k"))
 
 
 def fc_attention_workspace_bytes(d: AttnDesc, op: int) -> int:
@@ -694,18 +711,21 @@ def fc_attention_workspace_bytes(d: AttnDesc, op: int) -> int:
 
 def fc_attention_fwd(d: AttnDesc, seg, q, k, v, slope, pos_q, pos_k, out, lse, workspace, stream=None):
     """``seg`` is a ``Segments`` or None (one segment of all rows)."""
-    a = _Args(d.dtype, stream, workspace)
-    a.call(lib().fc_attention_fwd, *_attn_inputs(a, d, seg, q, k, v, slope, pos_q, pos_k),
-           a.data(out, (d.n_query, d.heads_q, d.head_dim), "out"), a.f32(lse, (d.n_query, d.heads_q), "lse"), a.ws,
-           a.ws_bytes)
+    import torch
+    dev, elem = _place(q, "q"), _elem(d.dtype)
+    _run(lib().fc_attention_fwd, dev, stream, *_attn_inputs(d, elem, dev, seg, q, k, v, slope, pos_q, pos_k),
+         _arr(out, elem, (d.n_query, d.heads_q, d.head_dim), dev, "out"),
+         _arr(lse, torch.float32, (d.n_query, d.heads_q), dev, "lse"), *_ws(workspace, dev))
 
 
 def fc_attention_vjp(d: AttnDesc, seg, q, k, v, slope, pos_q, pos_k, out, lse, g_out, q_grad, k_grad, v_grad,
                      slope_grad, pos_q_grad, pos_k_grad, workspace, stream=None):
-    a = _Args(d.dtype, stream, workspace)
+    import torch
+    dev, elem, f32 = _place(q, "q"), _elem(d.dtype), torch.float32
     qs, ks = (d.n_query, d.heads_q, d.head_dim), (d.n_key, d.heads_k, d.head_dim)
-    a.call(lib().fc_attention_vjp, *_attn_inputs(a, d, seg, q, k, v, slope, pos_q, pos_k), a.data(out, qs, "out"),
-           a.f32(lse, (d.n_query, d.heads_q), "lse"), a.data(g_out, qs, "g_out"), a.data(q_grad, qs, "q_grad"),
-           a.data(k_grad, ks, "k_grad"), a.data(v_grad, ks, "v_grad"), a.f32(slope_grad, (d.heads_q,), "slope_grad"),
-           a.f32(pos_q_grad, (d.n_query, 3), "pos_q_grad"), a.f32(pos_k_grad, (d.n_key, 3), "pos_k_grad"), a.ws,
-           a.ws_bytes)
+    _run(lib().fc_attention_vjp, dev, stream, *_attn_inputs(d, elem, dev, seg, q, k, v, slope, pos_q, pos_k),
+         _arr(out, elem, qs, dev, "out"), _arr(lse, f32, (d.n_query, d.heads_q), dev, "lse"),
+         _arr(g_out, elem, qs, dev, "g_out"), _arr(q_grad, elem, qs, dev, "q_grad"), _arr(k_grad, elem, ks, dev, "k_grad"),
+         _arr(v_grad, elem, ks, dev, "v_grad"), _arr(slope_grad, f32, (d.heads_q,), dev, "slope_grad"),
+         _arr(pos_q_grad, f32, (d.n_query, 3), dev, "pos_q_grad"), _arr(pos_k_grad, f32, (d.n_key, 3), dev, "pos_k_grad"),
+         *_ws(workspace, dev))
