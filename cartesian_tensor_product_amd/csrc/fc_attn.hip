@@ -116,17 +116,19 @@ struct PassPlan {
 };
 
 // `cols` columns and `rows` walked rows in all, over S segments; hk key heads.
-//  * kCols (four waves with a row tile in common) loads least.  It is taken
-//    where segments fill its 128 columns; long walks are split over blocks in
-//    parts of 1024 rows at least, while the chip has fewer than four blocks
-//    per CU.
-//  * Few columns over a long walk (single queries): four waves share the walk
-//    (kRows), and blocks in parts of 512 rows, up to two blocks per CU.
-//  * Few columns and rows (molecules): waves go alone (kOne).
-//  * The key pass of wide heads (one wave per SIMD for its registers) takes
-//    kRows also with many columns: with one wave, waiting for the three others
-//    at every tile costs more than the shared loads save (packed batch of 8192
-//    rows, 16 / 4 heads of 128: 215 us against 245 us).
+//  * kCols (four waves with a row tile in common) loads least, and is taken
+//    where its blocks of 128 columns, with the walk split in parts of 256 rows
+//    at least, fill the chip (one block per CU).  With a block per CU without
+//    it, only parts of 1024 rows are split off: partial results cost memory
+//    traffic.
+//  * Else four waves share the walk (kRows: four times the blocks; one segment
+//    of 939 rows, one head of 64 in fp32, forward and VJP: 269 us as kCols with
+//    8 blocks against 109 us), also split in parts of 256 rows.
+//  * Short walks (molecules): waves go alone (kOne).
+//  * The key pass of wide bfloat16 heads (one wave per SIMD for its registers)
+//    takes kRows also with many columns: with one wave, waiting for the three
+//    others at every tile costs more than the shared loads save (packed batch of
+//    8192 rows, 16 / 4 heads of 128: 215 us against 245 us).
 PassPlan plan_pass(const AttnArgs& a, bool is_bf16, AttnPass pass, int64_t cols, int64_t rows) {
   PassPlan p;
   const int64_t mean = (cols + a.S - 1) / a.S, walk = rows / a.S;
@@ -135,16 +137,19 @@ PassPlan plan_pass(const AttnArgs& a, bool is_bf16, AttnPass pass, int64_t cols,
   };
   p.hb = pass == kAttnFwd && a.slope && attn_two_heads(is_bf16, a.D) && a.hk % 2 == 0 && mean >= 32 ? 2 : 1;
   const int64_t units = (int64_t)a.S * (a.hk / p.hb);
-  if (pass == kAttnKey && is_bf16 && a.D > 64 && mean >= 96 && walk >= 1024) {
-    p.mode = kRows, p.splits = splits((mean + 31) / 32 * units, 4096, 2048);
-  } else if (mean >= 96 || attn_cols_only(is_bf16, a.D)) {
-    const int64_t blocks = (mean + 127) / 128 * units;
-    p.mode = kCols, p.splits = mean >= 96 ? splits(blocks, 960, 512 * 2 / p.hb) : splits(blocks, 512, 128);
-  } else if (walk >= 256) {
-    p.mode = kRows, p.splits = splits((mean + 31) / 32 * units, 512, 512);
-  } else {
-    p.mode = kOne, p.splits = 1;
+  const int64_t wide = (mean + 127) / 128 * units, narrow = (mean + 31) / 32 * units;
+  if (attn_cols_only(is_bf16, a.D)) {
+    p.mode = kCols, p.splits = splits(wide, 512, wide < 256 ? 128 : 1024);
+    return p;
   }
+  if (walk < 128) {
+    p.mode = mean >= 256 ? kCols : kOne, p.splits = 1;
+    return p;
+  }
+  p.mode = kCols, p.splits = wide < 256 ? splits(wide, 512, 256) : splits(wide, 960, 1024);
+  if (mean < 96 || wide * p.splits < 256) p.mode = kRows, p.splits = splits(narrow, 512, 256);
+  if (pass == kAttnKey && is_bf16 && a.D > 64 && p.mode == kCols)
+    p.mode = kRows, p.splits = splits(narrow, 4096, 2048);
   return p;
 }
 

@@ -17,6 +17,7 @@
 #include "fc_embed.h"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fc_types.h"
 
@@ -49,12 +50,10 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(int N, int R, int C, flo
 // ids as sort keys: padding sorts behind the last row
 __device__ __forceinline__ int key_of(int id, int R) { return id >= 0 && id < R ? id : R; }
 
-// counts of one digit per block, hist[digit][block]; the first pass also
-// clears the run bounds of every row
+// counts of one digit per block, hist[digit][block]
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(int N, int R, int shift, int ndig, bool first_pass,
                                                                   const int* __restrict__ keys,
-                                                                  int* __restrict__ hist, int* __restrict__ first,
-                                                                  int* __restrict__ last) {
+                                                                  int* __restrict__ hist) {
   __shared__ int cnt[256];
   const int t = threadIdx.x;
   cnt[t] = 0;
@@ -70,12 +69,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(int N, int R, 
   }
   __syncthreads();
   if (t < ndig) hist[(size_t)t * gridDim.x + blockIdx.x] = cnt[t];
-  if (first_pass)
-    for (int r = blockIdx.x * kSortThreads + t; r < R; r += gridDim.x * kSortThreads) first[r] = last[r] = 0;
 }
 
-// exclusive scan over the blocks of one digit (one block per digit)
-__global__ __launch_bounds__(256) void sort_scan_kernel(int nblk, int* __restrict__ hist, int* __restrict__ total) {
+// exclusive scan over the blocks of one digit (one block per digit); the
+// grid also clears the run bounds of R rows (0 but in the first pass)
+__global__ __launch_bounds__(256) void sort_scan_kernel(int nblk, int* __restrict__ hist, int* __restrict__ total,
+                                                        int R, int* __restrict__ first, int* __restrict__ last) {
   __shared__ int sums[4];
   const int t = threadIdx.x, lane = t % 64, w = t / 64;
   int* h = hist + (size_t)blockIdx.x * nblk;
@@ -101,6 +100,7 @@ __global__ __launch_bounds__(256) void sort_scan_kernel(int nblk, int* __restric
     __syncthreads();
   }
   if (t == 0) total[blockIdx.x] = carry;
+  for (int r = blockIdx.x * 256 + t; r < R; r += gridDim.x * 256) first[r] = last[r] = 0;
 }
 
 // Stable scatter: a wave takes 64 neighbouring keys at a time, finds the
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(int N, int R, int C, int
 // grid apart, so that neighbouring frequent rows (tables are often ordered by
 // frequency) fall to different blocks.  Rows of more than kLong pieces
 // are left to the whole block, whose waves take pieces in turn and add up in
-// wave order.
+// wave order.  gridDim.y blocks share the channels.
 constexpr int kLong = 16;
 template <int W, int RW, int V>
 __global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int chunk, float scale,
@@ -281,6 +281,7 @@ __global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int ch
   __shared__ float sum[W][64 * V];
   __shared__ int bound[2][ROWS];
   const int w = threadIdx.x / 64, lane = threadIdx.x % 64;
+  const int c_begin = blockIdx.y * 64 * V, c_step = gridDim.y * 64 * V;
   auto row = [&](int i) { return (int)(blockIdx.x + i * gridDim.x); };
   const int rows = (R - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // at most ROWS
   for (int i = threadIdx.x; i < rows; i += W * 64) bound[0][i] = first[row(i)], bound[1][i] = last[row(i)];
@@ -293,7 +294,7 @@ __global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int ch
     const bool is_long = l > f && b - a >= kLong;
     any_long |= is_long;
     if (i / (RW == 1 ? W : RW) != w || is_long || (l > f && a == b)) continue;
-    for (int c = lane * V; c < C; c += 64 * V) {
+    for (int c = c_begin + lane * V; c < C; c += c_step) {
       float acc[V] = {};
       for (int ch = a; l > f && ch <= b; ++ch) {
         float x[V];
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int ch
   for (int i = 0; i < rows; ++i) {
     const int f = bound[0][i], l = bound[1][i], a = f / chunk, b = (l - 1) / chunk;
     if (l <= f || b - a < kLong) continue;
-    for (int c0 = 0; c0 < C; c0 += 64 * V) {
+    for (int c0 = c_begin; c0 < C; c0 += c_step) {
       const int c = c0 + lane * V;
       float acc[V] = {};
       if (c < C) {
@@ -347,8 +348,20 @@ int pow2_at_least(int n) {
 
 // channels per lane: 16 bytes of the element type where rows allow it
 int vec_of(int C, bool bf16, bool aligned) {
-  const int v = bf16 ? 8 : 4;
-  return aligned && C % v == 0 ? v : 1;
+  int v = aligned ? bf16 ? 8 : 4 : 1;
+  while (C % v != 0) v >>= 1;
+  return v;
+}
+
+template <class F>
+void dispatch(bool is_bf16, int vec, F&& f) {
+  auto type = [&](auto v) { is_bf16 ? f(bf16{}, v) : f(float{}, v); };
+  switch (vec) {
+    case 8: f(bf16{}, std::integral_constant<int, 8>{}); break;
+    case 4: type(std::integral_constant<int, 4>{}); break;
+    case 2: type(std::integral_constant<int, 2>{}); break;
+    default: type(std::integral_constant<int, 1>{}); break;
+  }
 }
 
 template <class T, int V>
@@ -371,7 +384,8 @@ void sum_t(const EmbedPlan& p, float scale, const int* key, const int* ord, cons
 template <int W, int RW, int V>
 void join_t(const EmbedPlan& p, float scale, float* grad, hipStream_t st) {
   constexpr int rows = RW == 1 ? 1 : W * RW;
-  hipLaunchKernelGGL((embed_join_kernel<W, RW, V>), dim3((p.R + rows - 1) / rows), dim3(W * 64), 0, st, p.R, p.C,
+  const int y = RW == 1 ? (p.C + 64 * V - 1) / (64 * V) : 1;
+  hipLaunchKernelGGL((embed_join_kernel<W, RW, V>), dim3((p.R + rows - 1) / rows, y), dim3(W * 64), 0, st, p.R, p.C,
                      p.chunk, scale, p.first, p.last, p.part, grad);
 }
 
@@ -416,11 +430,9 @@ EmbedPlan embed_plan(int N, int R, int C, bool bf16, bool aligned, void* ws) {
 
 void launch_embed_fwd(int N, int R, int C, bool is_bf16, bool aligned, float scale, const void* table, const int* ids,
                       void* out, hipStream_t st) {
-  const int v = vec_of(C, is_bf16, aligned);
-  if (is_bf16)
-    v > 1 ? fwd_t<bf16, 8>(N, R, C, scale, table, ids, out, st) : fwd_t<bf16, 1>(N, R, C, scale, table, ids, out, st);
-  else
-    v > 1 ? fwd_t<float, 4>(N, R, C, scale, table, ids, out, st) : fwd_t<float, 1>(N, R, C, scale, table, ids, out, st);
+  dispatch(is_bf16, vec_of(C, is_bf16, aligned), [&](auto t, auto v) {
+    fwd_t<decltype(t), decltype(v)::value>(N, R, C, scale, table, ids, out, st);
+  });
 }
 
 void launch_embed_vjp(const EmbedPlan& p, bool is_bf16, float scale, const int* ids, const void* g, float* grad,
@@ -431,22 +443,23 @@ void launch_embed_vjp(const EmbedPlan& p, bool is_bf16, float scale, const int* 
   for (int s = 0; s < p.passes; ++s) {
     int *ko = p.key[s & 1], *oo = p.ord[s & 1];
     hipLaunchKernelGGL(sort_count_kernel, dim3(p.sort_blocks), dim3(kSortThreads), 0, st, p.N, p.R, s * p.bits, ndig,
-                       s == 0, key, p.hist, p.first, p.last);
-    hipLaunchKernelGGL(sort_scan_kernel, dim3(ndig), dim3(256), 0, st, p.sort_blocks, p.hist, p.total);
+                       s == 0, key, p.hist);
+    hipLaunchKernelGGL(sort_scan_kernel, dim3(ndig), dim3(256), 0, st, p.sort_blocks, p.hist, p.total,
+                       s == 0 ? p.R : 0, p.first, p.last);
     hipLaunchKernelGGL(sort_scatter_kernel, dim3(p.sort_blocks), dim3(kSortThreads), 0, st, p.N, p.R, s * p.bits,
                        p.bits, s == 0, key, ord, p.hist, p.total, ko, oo);
     key = ko;
     ord = oo;
   }
-  if (is_bf16)
-    p.vec > 1 ? sum_t<bf16, 8>(p, scale, key, ord, g, grad, st) : sum_t<bf16, 1>(p, scale, key, ord, g, grad, st);
+  dispatch(is_bf16, p.vec, [&](auto t, auto v) {
+    sum_t<decltype(t), decltype(v)::value>(p, scale, key, ord, g, grad, st);
+  });
+  // few rows, whose runs are long: a block of 16 waves for each and 64
+  // channels; many: each wave a run of rows
+  if (p.R <= 512)
+    join_t<16, 1, 1>(p, scale, grad, st);
   else
-    p.vec > 1 ? sum_t<float, 4>(p, scale, key, ord, g, grad, st) : sum_t<float, 1>(p, scale, key, ord, g, grad, st);
-  // few rows: a block of 16 waves for each; many: each wave a run of rows
-  if (p.R <= 4096)
-    p.vec > 1 ? join_t<16, 1, 4>(p, scale, grad, st) : join_t<16, 1, 1>(p, scale, grad, st);
-  else
-    p.vec > 1 ? join_t<4, 8, 4>(p, scale, grad, st) : join_t<4, 8, 1>(p, scale, grad, st);
+    p.vec >= 4 ? join_t<4, 8, 4>(p, scale, grad, st) : join_t<4, 8, 1>(p, scale, grad, st);
 }
 
 }  // namespace fc
