@@ -243,12 +243,15 @@ void sum_splits(bool is_bf16, int n, int width, int S, const int* seg, int split
 }  // namespace
 
 size_t attn_workspace_bytes(const AttnArgs& a, bool is_bf16, int op) {
-  // the largest a call of this descriptor can need: every gradient wanted
+  // the largest a call of this descriptor can need: with slopes and every
+  // gradient, or without slopes (whose forward may split the keys further)
   AttnArgs b = a;
   static const float some = 0.f;
+  b.slope = b.g_slope = nullptr;
+  const size_t without = make_plan(b, is_bf16, op, nullptr).bytes;
   b.slope = &some;
   b.g_slope = const_cast<float*>(&some);
-  return make_plan(b, is_bf16, op, nullptr).bytes;
+  return std::max(without, make_plan(b, is_bf16, op, nullptr).bytes);
 }
 
 void launch_attn_fwd(const AttnArgs& a, bool is_bf16, void* ws, hipStream_t st) {

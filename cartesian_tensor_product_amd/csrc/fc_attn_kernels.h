@@ -153,7 +153,8 @@ struct Tile {
   }
 
   // out[d][col] += sum_row rows[row][d] w[row][col] for 32 rows in LDS; the
-  // weights are split as the rows are (bfloat16: rounded)
+  // weights are taken as WP parts
+  template <int WP>
   static __device__ __forceinline__ void outer(const bf16* rows, const f32x16& w, f32x16 (&out)[DB], int lane) {
     // 16 lanes read four rows x 16 columns and get a column each
     const bf16* p = rows + ((lane / 32) * 4 + (lane % 16) / 4) * LD + ((lane / 16) % 2) * 16 + (lane % 4) * 4;
@@ -163,7 +164,7 @@ struct Tile {
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = w[8 * s + i];
-      bf16x8 wb[NP];
+      bf16x8 wb[WP];
       split(x, wb);
 #pragma unroll
       for (int b = 0; b < DB; ++b) {
@@ -176,6 +177,7 @@ struct Tile {
           a[k] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
         if constexpr (NP == 3) out[b] = mma_low(a, wb, out[b]);
+        if constexpr (WP == 2) out[b] = mma(a[0], wb[1], out[b]);
         out[b] = mma(a[0], wb[0], out[b]);
       }
     }
@@ -253,17 +255,18 @@ __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32);
 __device__ __forceinline__ f32x4 four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 
 // The capped score cap tanh(u / cap) / log 2 - ref of a raw product, and the
-// derivative's factor 1 - tanh^2.  bfloat16 rows: with w = 1 / (1 + exp(2 u /
-// cap)) it is c2 - ref - 2 c2 w, and the factor 4 w (1 - w); the error is that
-// of w, a few 2^-24 cap.  fp32 rows: tanh within a few 2^-24 of its value also
-// near 0, where w alone would lose digits.
-template <class T>
+// derivative's factor 1 - tanh^2.  EXACT: tanh within a few 2^-24 of its value
+// also near 0.  Else, with w = 1 / (1 + exp(2 u / cap)), it is c2 - ref - 2 c2 w,
+// and the factor 4 w (1 - w): a third of the work, for an error of a few 2^-24
+// cap, which is taken where bfloat16 weights are rounded to 2^-9 anyway
+// (kWeightParts of 1).
+template <bool EXACT>
 struct Cap {
-  float c1, c2;   // scale / cap (bfloat16: times 2 / log 2), cap / log 2
+  float c1, c2;   // scale / cap (else: times 2 / log 2), cap / log 2
   __device__ __forceinline__ Cap(float scale, float cap)
-      : c1(scale / cap * (sizeof(T) == 2 ? 2.f * kLog2e : 1.f)), c2(cap * kLog2e) {}
+      : c1(scale / cap * (!EXACT ? 2.f * kLog2e : 1.f)), c2(cap * kLog2e) {}
   __device__ __forceinline__ float score(float u, float ref, float& t) const {
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (!EXACT) {
       t = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u * c1));
       return fmaf(-2.f * c2, t, c2 - ref);
     } else {
@@ -278,12 +281,12 @@ struct Cap {
       return fmaf(c2, t, -ref);
     }
   }
-  // ds (1 - tanh^2), for bfloat16 without the 4 (Cap::kRest)
+  // ds (1 - tanh^2), without kRest
   static __device__ __forceinline__ float slope(float ds, float t) {
-    if constexpr (sizeof(T) == 2) return ds * fmaf(-t, t, t);
+    if constexpr (!EXACT) return ds * fmaf(-t, t, t);
     return fmaf(-t * t, ds, ds);
   }
-  static constexpr float kRest = sizeof(T) == 2 ? 4.f : 1.f;
+  static constexpr float kRest = !EXACT ? 4.f : 1.f;
 };
 
 // 1 / r of a squared distance.  Squares carry 1e-35, so that at r = 0 this is
@@ -449,6 +452,17 @@ struct Waves {
   }
 };
 
+// Parts of the weights (P, dS) in the second products of bfloat16 rows.  One is
+// a rounding of 2^-9 at most to each weight, as large as the output's own.  Two
+// bring it down to 2^-17 for one matrix instruction and a split more, which costs
+// nothing where a call is bound by latency or its loads (kOne, kRows: 16 rows
+// over 16 .. 8192 keys 32.2 us with one part, 33.2 us with two), but 15 to 25 %
+// where the vector units are full (kCols: 16384 rows, 8 heads of 64 with slopes
+// 1.01 ms and 1.27 ms).  Wide heads of the key pass run as kRows under full
+// load, too.
+template <class T, int DP, int MODE, bool KEY = false>
+constexpr int kWeightParts = sizeof(T) == 4 ? 3 : MODE == kCols || (KEY && DP > 64) ? 1 : 2;
+
 // ------------------------------------------------- results of a wave's columns --
 
 // out(hb, d, x): four elements from d of head hb, for the lane's column
@@ -542,6 +556,7 @@ __global__ __launch_bounds__(Waves<MODE>::TH, (waves_per_simd<T, DP, HB, MODE, B
 void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
   using TL = Tile<T, DP, HB>;
   using WV = Waves<MODE>;
+  constexpr int WP = kWeightParts<T, DP, MODE>;
   constexpr int ROWS = fwd_rows<T, HB, MODE>(), NS = ROWS / 32;
   constexpr int AREA = ROWS * TL::LD * TL::NP;   // LDS of one row tile
   __shared__ __align__(16) bf16 lds[WV::REGIONS * 2 * AREA];
@@ -599,7 +614,7 @@ void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
   float px = 0.f, py = 0.f, pz = 0.f;
   if (BIAS && live) px = a.pos_q[3 * qrow], py = a.pos_q[3 * qrow + 1], pz = a.pos_q[3 * qrow + 2];
   const float c1 = a.scale * kLog2e;
-  const Cap<T> cap(a.scale, a.cap);
+  const Cap<(WP > 1)> cap(a.scale, a.cap);
 
   bool first = true;
   auto tile = [&](bool edge, int j0) {
@@ -691,7 +706,7 @@ void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
           sum += s[hb][n][r];
         }
         l[hb] += sum;
-        TL::outer(lv + n * TL::NP * TL::PART + hb * DP, s[hb][n], o[hb], lane);
+        TL::template outer<WP>(lv + n * TL::NP * TL::PART + hb * DP, s[hb][n], o[hb], lane);
       }
   };
   for (int j0 = kb; j0 < ke; j0 += ROWS * WV::STRIDE) {
@@ -761,11 +776,15 @@ void attn_fwd_kernel(AttnArgs a, AttnPart part, int tiles) {
 // DELTA: only delta_i = sum_j P dP into part.delta.  Else q_bar, and the
 // position and slope gradients of the query rows into part.row; delta comes
 // from the delta pass, or is <g, out>, formed here and left for the key pass.
+// A row that sees no more than one tile takes it as the mean of dP there: with
+// few keys dP - delta is small beside both, and <g, out> has out's rounding.
+// (So a row of one key has dS = 0, not a rest.)
 template <class T, int DP, int MODE, bool BIAS, bool CAP, bool DELTA>
 __global__ __launch_bounds__(Waves<MODE>::TH, (waves_per_simd<T, DP, 1, MODE, BIAS>(2, !DELTA, 2 + BIAS, 32)))
 void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
   using TL = Tile<T, DP, 1>;
   using WV = Waves<MODE>;
+  constexpr int WP = kWeightParts<T, DP, MODE>;
   constexpr int ROWS = 32;
   constexpr int AREA = ROWS * TL::LD * TL::NP;   // LDS of one row tile
   __shared__ __align__(16) bf16 lds[WV::REGIONS * 2 * AREA];
@@ -815,14 +834,17 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
   TL::load_cols(static_cast<const T*>(a.g) + (live ? orow * a.D : 0), live, a.D, h, gf);
   const float slope = BIAS && live ? a.slope[head] * kLog2e : 0.f;
   const Norm norm(live ? a.lse[orow] : -kInf);   // the factor is the column's own: at the end
+  // delta of a column that sees at most one tile is formed there (below); only
+  // split 0 (wave 0) meets that tile, and writes part.delta after it
+  const bool brief = vis <= ROWS;
   float delta = 0.f;
   if constexpr (!DELTA) {
     if (part.exact) {
-      if (live)
+      if (!brief)
         for (int s = 0; s < part.dsplits; ++s) delta += part.delta[s * nrows + orow];
     } else {
       // the lane's elements of both rows, as load_cols takes them
-      for (int d = 8 * h; live && d < a.D; d += 16) {
+      for (int d = 8 * h; !brief && d < a.D; d += 16) {
         float x[8], y[8];
         load_f32<T, 8>(static_cast<const T*>(a.out) + orow * a.D + d, x);
         load_f32<T, 8>(static_cast<const T*>(a.g) + orow * a.D + d, y);
@@ -830,7 +852,7 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
         for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
       }
       delta += other_half(delta);
-      if (lead && w.split == 0) part.delta[orow] = delta;
+      if (lead && !brief && w.split == 0) part.delta[orow] = delta;
     }
   }
 #pragma unroll
@@ -838,7 +860,7 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
   float px = 0.f, py = 0.f, pz = 0.f;
   if (BIAS && live) px = a.pos_q[3 * qrow], py = a.pos_q[3 * qrow + 1], pz = a.pos_q[3 * qrow + 2];
   const float c1 = a.scale * kLog2e;
-  const Cap<T> cap(a.scale, a.cap);
+  const Cap<(WP > 1)> cap(a.scale, a.cap);
   float v[4] = {0.f, 0.f, 0.f, 0.f}, dsum[1] = {0.f};   // position and slope gradients; delta
 
   auto tile = [&](bool edge, int j0) {
@@ -851,26 +873,55 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
       for (int r = 0; r < 16; ++r)
         if (acc_row(r, h) >= last) s[r] = -kInf;
     }
+    // weight of register r, element e of the points pt, relative to 2^-ref;
+    // its tanh, distance and inverse distance
+    auto weight = [&](int r, int e, const Points& pt, float& th, float& d, float& inv) {
+      float x;
+      if constexpr (CAP) {
+        x = cap.score(s[r], norm.ref, th);
+        if ((BIAS || DELTA) && edge && j0 + acc_row(r, h) >= vis) x = -kInf;
+      } else {
+        x = fmaf(s[r], c1, -norm.ref);
+      }
+      if constexpr (BIAS) {
+        inv = inv_dist(pt.square(e));
+        d = dist_of<T>(pt.square(e), inv);
+        x = fmaf(-slope, d, x);
+      }
+      return __builtin_amdgcn_exp2f(x);
+    };
+    auto points = [&](int r4) {
+      const float* p = lp + (BIAS ? r4 * 8 + h * 4 : 0);
+      return Points(px, py, pz, p, BIAS ? p + ROWS : p, BIAS ? p + 2 * ROWS : p);
+    };
+    if constexpr (!DELTA)
+      if (j0 == 0 && __any(live && brief)) {
+        // the mean of dP, from the first key's on
+        const float dp0 = __shfl(dp[0], lane % 32);
+        float sum = 0.f, more = 0.f;
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const Points pt = points(r4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = r4 * 4 + e;
+            float th, d, inv;
+            const float pr = weight(r, e, pt, th, d, inv);
+            if (acc_row(r, h) < vis) sum += pr, more = fmaf(pr, dp[r] - dp0, more);
+          }
+        }
+        sum += other_half(sum);
+        more += other_half(more);
+        if (brief && sum > 0.f) delta = dp0 + more / sum;
+      }
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
-      const float* p = lp + (BIAS ? r4 * 8 + h * 4 : 0);
-      const Points pt(px, py, pz, p, BIAS ? p + ROWS : p, BIAS ? p + 2 * ROWS : p);
+      const Points pt = points(r4);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = r4 * 4 + e;
-        float th = 0.f, x, inv, d;
-        if constexpr (CAP) {
-          x = cap.score(s[r], norm.ref, th);
-          if ((BIAS || DELTA) && edge && j0 + acc_row(r, h) >= vis) x = -kInf;
-        } else {
-          x = fmaf(s[r], c1, -norm.ref);
-        }
-        if constexpr (BIAS) {
-          inv = inv_dist(pt.square(e));
-          d = dist_of<T>(pt.square(e), inv);
-          x = fmaf(-slope, d, x);
-        }
-        const float pr = __builtin_amdgcn_exp2f(x);
+        float th = 0.f, d = 0.f, inv = 0.f;
+        const float pr = weight(r, e, pt, th, d, inv);
         if constexpr (DELTA) {
           gd = fmaf(pr, dp[r], gd);
         } else {
@@ -879,7 +930,7 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
             gs = fmaf(ds, d, gs);
             pt.add(e, ds * inv, gp);   // the slope is the column's own: at the end
           }
-          if constexpr (CAP) ds = Cap<T>::slope(ds, th);
+          if constexpr (CAP) ds = Cap<(WP > 1)>::slope(ds, th);
           s[r] = ds;
         }
       }
@@ -892,7 +943,7 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
     }
     if constexpr (DELTA) dsum[0] += gd;
     if constexpr (BIAS && !DELTA) v[0] += gp[0], v[1] += gp[1], v[2] += gp[2], v[3] += gs;
-    if constexpr (!DELTA) TL::outer(lk, s, dq[0], lane);
+    if constexpr (!DELTA) TL::template outer<WP>(lk, s, dq[0], lane);
   };
   for (int j0 = kb; j0 < ke; j0 += ROWS * WV::STRIDE) {
     WV::sync();
@@ -912,6 +963,7 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
     if (lead) part.delta[w.split * nrows + orow] = dsum[0];
     return;
   }
+  if (lead && brief && w.split == 0) part.delta[orow] = delta;
   if constexpr (BIAS) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = (v[c] + other_half(v[c])) * norm.factor;
@@ -923,7 +975,7 @@ void attn_query_kernel(AttnArgs a, AttnPart part, int tiles) {
 #pragma unroll
   for (int b = 0; b < TL::DB; ++b)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dq[0][b][r] *= norm.factor * (CAP ? Cap<T>::kRest : 1.f);
+    for (int r = 0; r < 16; ++r) dq[0][b][r] *= norm.factor * (CAP ? Cap<(WP > 1)>::kRest : 1.f);
   auto put = [&](size_t row, int d, const float* x) {
     const float y[4] = {x[0] * a.scale, x[1] * a.scale, x[2] * a.scale, x[3] * a.scale};
     if (part.splits == 1)
@@ -958,6 +1010,7 @@ __global__ __launch_bounds__(Waves<MODE>::TH, (waves_per_simd<T, DP, 1, MODE, BI
 void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
   using TL = Tile<T, DP, 1>;
   using WV = Waves<MODE>;
+  constexpr int WP = kWeightParts<T, DP, MODE, true>;
   constexpr int ROWS = 32;
   constexpr int AREA = ROWS * TL::LD * TL::NP;   // LDS of one row tile
   __shared__ __align__(16) bf16 lds[WV::REGIONS * 2 * AREA];
@@ -1041,21 +1094,25 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
   float px = 0.f, py = 0.f, pz = 0.f;
   if (BIAS && live) px = a.pos_k[3 * krow], py = a.pos_k[3 * krow + 1], pz = a.pos_k[3 * krow + 2];
   const float c1 = a.scale * kLog2e;
-  const Cap<T> cap(a.scale, a.cap);
+  const Cap<(WP > 1)> cap(a.scale, a.cap);
   float gp[3] = {0.f, 0.f, 0.f};
 
   auto tile = [&](bool edge) {
     float gt[3] = {0.f, 0.f, 0.f};   // of this tile
     f32x16 s = TL::dot(lq, kf, lane);
     f32x16 dp = TL::dot(lg, vf, lane);
-    if (edge && !CAP) {
+    if (edge) {
       const int jj = opaque(j);
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
         const i32x4 vis = *reinterpret_cast<const i32x4*>(lr.vis + r4 * 8 + h * 4);
+        const f32x4 delta = four(lr.delta + r4 * 8 + h * 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (jj >= vis[e]) s[r4 * 4 + e] = -kInf;
+        for (int e = 0; e < 4; ++e) {
+          const int r = r4 * 4 + e;
+          if (!CAP && jj >= vis[e]) s[r] = -kInf;
+          if (vis[e] == 1) dp[r] = delta[e];   // dS of a row with one key: 0
+        }
       }
     }
 #pragma unroll
@@ -1084,7 +1141,7 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
         const float p = __builtin_amdgcn_exp2f(x) * factor[e];
         float ds = p * (dp[r] - delta[e]);
         if constexpr (BIAS) pt.add(e, ds * inv * sl[e], gt);
-        if constexpr (CAP) ds = Cap<T>::slope(ds, th);
+        if constexpr (CAP) ds = Cap<(WP > 1)>::slope(ds, th);
         s[r] = p;
         dp[r] = ds;
       }
@@ -1100,8 +1157,8 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
       }
     }
     if constexpr (BIAS) gp[0] += gt[0], gp[1] += gt[1], gp[2] += gt[2];
-    TL::outer(lg, s, dv[0], lane);
-    TL::outer(lq, dp, dk[0], lane);
+    TL::template outer<WP>(lg, s, dv[0], lane);
+    TL::template outer<WP>(lq, dp, dk[0], lane);
   };
   for (int r0 = rb; r0 < re; r0 += step * WV::STRIDE) {
     WV::sync();
@@ -1153,7 +1210,7 @@ void attn_key_kernel(AttnArgs a, AttnPart part, int tiles) {
       });
     }
   };
-  write(dk, a.gk, part.o, a.scale * (CAP ? Cap<T>::kRest : 1.f));
+  write(dk, a.gk, part.o, a.scale * (CAP ? Cap<(WP > 1)>::kRest : 1.f));
   write(dv, a.gv, part.o2, 1.f);
 }
 

@@ -121,10 +121,10 @@ class Case:
             dP = g[A, h] @ v[B, kh].T
             edP = (self.D + 2) * U * np.abs(g[A, h]) @ np.abs(v[B, kh]).T
             delta = (P * dP).sum(1, keepdims=True)
-            if rho and bias:   # delta from the scores
-                ed = (P * (np.abs(dP) * (eP + (lk + 2) * U) + edP)).sum(1, keepdims=True)
-            else:              # delta from out
-                ed = (np.abs(g[A, h]) * (b["out"][A, h] + (self.D + 2) * U * np.abs(want_out[A, h]))).sum(1, keepdims=True)
+            # delta: from the scores, also of rows that see few keys, or from out
+            scores = (P * (np.abs(dP) * (eP + (lk + 2) * U) + edP)).sum(1, keepdims=True)
+            out = (np.abs(g[A, h]) * (b["out"][A, h] + (self.D + 2) * U * np.abs(want_out[A, h]))).sum(1, keepdims=True)
+            ed = scores if rho and bias else np.where(see.sum(1, keepdims=True) <= 32, scores, out)
             dS = P * (dP - delta)
             edS = np.abs(dS) * (eP + 4 * U) + P * (edP + ed)
             n = lq * lk
@@ -223,6 +223,27 @@ def test_single_queries_over_many_keys(dtype, bias):
 def test_few_keys_under_many_queries(dtype):
     """The walk over queries is split and joined."""
     Case(dtype, (2000, 900), (2, 5), hq=4, hk=2, D=32, bias=True, seed=5).check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("lens_q,lens_k,causal", [((1, 1), None, True), ((5, 0, 1, 70), (1, 1, 1, 1), False), ((300,), (1,), False)])
+def test_rows_of_one_key(dtype, cap, bias, lens_q, lens_k, causal):
+    """Their probability is 1 whatever the score: no score gradient, not a rounding's rest."""
+    c = Case(dtype, lens_q, lens_k, hq=4, hk=2, D=48, cap=cap, bias=bias, causal=causal)
+    grads = c.vjp(*c.fwd())
+    for name, x in grads.items():
+        assert name == "v" or not x.any(), name
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens", [(2,), (2, 3, 9, 32), (33, 40)])
+def test_causal_rows_of_few_keys(dtype, lens):
+    """Differences dP - delta far below dP."""
+    Case(dtype, lens, hq=4, hk=1, D=128, causal=True, cap=20.0).check()
+    Case(dtype, lens, hq=2, hk=2, D=64, causal=True, scale=1.0).check()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
