@@ -294,7 +294,7 @@ void launch_attn_vjp(const AttnArgs& a, bool is_bf16, void* ws, hipStream_t st) 
          a.g_slope ? p.slope : nullptr);
   if (a.g_pos_k && a.nk > 0)
     rows(a.nk, a.seg_k, a.hk, p.key.splits, p.pk.col, 0, 0, nullptr, a.g_pos_k, nullptr);
-  if (a.g_slope) launch_column_sum(p.slope_blocks, a.hq, p.slope, a.g_slope, st);
+  if (a.g_slope) launch_column_sum(p.slope_blocks, a.hq, p.slope, a.g_slope, nullptr, st);
 }
 
 }  // namespace fc

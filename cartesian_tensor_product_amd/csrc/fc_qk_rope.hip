@@ -23,7 +23,8 @@
 namespace fc {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;      // of a block
+constexpr int kVjpWaves = 4;   // per SIMD in the VJP: a thousand blocks at once
 
 // Work of a lane: V pair slots from `slot`; P groups share a node.
 struct Lane {
@@ -70,6 +71,24 @@ __device__ __forceinline__ void load_pairs(const T* p, int a, int b, float* x1, 
   }
 }
 
+// the same in two steps: the pieces on their way, and their values
+template <class T, int V>
+struct Pieces {
+  Pack<T, V> a, b;
+  __device__ __forceinline__ void load(const T* p, int at_a, int at_b) {
+    a = *reinterpret_cast<const Pack<T, V>*>(p + at_a);
+    b = *reinterpret_cast<const Pack<T, V>*>(p + at_b);
+  }
+  template <bool INTER>
+  __device__ __forceinline__ void get(float* x1, float* x2) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      x1[i] = static_cast<float>(INTER ? (2 * i < V ? a : b).e[2 * i % V] : a.e[i]);
+      x2[i] = static_cast<float>(INTER ? (2 * i + 1 < V ? a : b).e[(2 * i + 1) % V] : b.e[i]);
+    }
+  }
+};
+
 template <class T, int V, bool INTER>
 __device__ __forceinline__ void store_pairs(T* p, int a, int b, const float* x1, const float* x2) {
   if constexpr (INTER) {
@@ -94,8 +113,23 @@ __device__ __forceinline__ void turn(const float (*freq)[3], const float* pos, f
   }
 }
 
+// v of the lane that the data-parallel control names (all lanes are active)
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over `group` neighbouring lanes (a power of two, the same for the wave).
+// Up to 16 lanes by moves inside the vector unit: neighbours, pairs, then the
+// mirrored half of 8 and of 16, whose lanes hold equal sums by then.  (Through
+// LDS, as shuffles go, each step is a round trip that nothing else fills.)
 __device__ __forceinline__ float group_sum(float v, int group) {
-  for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if (group > 1) v += moved<0xb1>(v);
+  if (group > 2) v += moved<0x4e>(v);
+  if (group > 4) v += moved<0x141>(v);
+  if (group > 8) v += moved<0x140>(v);
+  if (group > 16) v += __shfl_xor(v, 16);
+  if (group > 32) v += __shfl_xor(v, 32);
   return v;
 }
 
@@ -163,7 +197,7 @@ __global__ __launch_bounds__(kWaves * 64) void qk_rope_fwd_kernel(QkRopeArgs A, 
 // Nodes in turn; a lane keeps the gamma gradients of its elements over all of
 // its nodes and heads in registers.
 template <class T, int V, bool INTER>
-__global__ __launch_bounds__(kWaves * 64) void qk_rope_vjp_kernel(QkRopeArgs A, int group, int share) {
+__global__ __launch_bounds__(kWaves * 64, kVjpWaves) void qk_rope_vjp_kernel(QkRopeArgs A, int group, int share) {
   __shared__ float lds[kWaves][2][kQkMaxDim];
   Lane l = lane_of<V>(A.D, group, share);
   int a, b;
@@ -183,15 +217,24 @@ __global__ __launch_bounds__(kWaves * 64) void qk_rope_vjp_kernel(QkRopeArgs A, 
     auto heads = [&](const T* x, int64_t stride, int H, const float* gamma, const T* g, T* xb, float (*gm)[V]) {
       float w1[V], w2[V];
       load_gamma<V, INTER>(gamma, l, a, b, w1, w2);
+      Pieces<T, V> px = {}, pg = {};
+      auto fetch = [&](int h) {
+        if (!live || h >= H) return;
+        px.load(x + (size_t)n * stride + (size_t)h * A.D, a, b);
+        pg.load(g + ((size_t)n * H + h) * A.D, a, b);
+      };
+      fetch(l.head0);
       for (int h0 = 0; h0 < H; h0 += share) {
         const int h = h0 + l.head0;
         const bool on = live && h < H;
-        float x1[V] = {}, x2[V] = {}, g1[V] = {}, g2[V] = {};
         const size_t row = ((size_t)n * H + h) * A.D;
-        if (on) {
-          load_pairs<T, V, INTER>(x + (size_t)n * stride + (size_t)h * A.D, a, b, x1, x2);
-          load_pairs<T, V, INTER>(g + row, a, b, g1, g2);
-        }
+        float x1[V], x2[V], g1[V], g2[V];
+        px.template get<INTER>(x1, x2);
+        pg.template get<INTER>(g1, g2);
+        if (!on)
+#pragma unroll
+          for (int i = 0; i < V; ++i) x1[i] = x2[i] = g1[i] = g2[i] = 0.f;
+        fetch(h + share);
         float q = 0.f, d = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -285,7 +328,7 @@ Shape shape_of(const QkRopeArgs& a, int vec) {
   return s;
 }
 
-template <class F>
+template <int MOST, class F>
 void dispatch(const QkRopeArgs& a, int vec, F&& f) {
   auto inter = [&](auto t, auto v) {
     a.interleaved ? f(t, v, std::integral_constant<bool, true>{}) : f(t, v, std::integral_constant<bool, false>{});
@@ -298,7 +341,9 @@ void dispatch(const QkRopeArgs& a, int vec, F&& f) {
     }
   };
   switch (vec) {
-    case 8: type(std::integral_constant<int, 8>{}); break;
+    case 8:
+      if constexpr (MOST == 8) type(std::integral_constant<int, 8>{});
+      break;
     case 4: type(std::integral_constant<int, 4>{}); break;
     case 2: type(std::integral_constant<int, 2>{}); break;
     default: type(std::integral_constant<int, 1>{}); break;
@@ -316,7 +361,7 @@ int qk_rope_vjp_blocks(const QkRopeArgs& a) {
 void launch_qk_rope_fwd(const QkRopeArgs& a, hipStream_t st) {
   const int vec = pairs_per_lane(a, false);
   const Shape s = shape_of(a, vec);
-  dispatch(a, vec, [&](auto t, auto v, auto inter) {
+  dispatch<8>(a, vec, [&](auto t, auto v, auto inter) {
     hipLaunchKernelGGL((qk_rope_fwd_kernel<decltype(t), decltype(v)::value, decltype(inter)::value>),
                        dim3((s.waves + kWaves - 1) / kWaves), dim3(kWaves * 64), 0, st, a, s.group, s.share);
   });
@@ -326,12 +371,11 @@ void launch_qk_rope_vjp(const QkRopeArgs& a, float* gamma_q_grad, float* gamma_k
   const int vec = pairs_per_lane(a, true);
   const Shape s = shape_of(a, vec);
   const int blocks = std::min((s.waves + kWaves - 1) / kWaves, qk_rope_vjp_blocks(a));
-  dispatch(a, vec, [&](auto t, auto v, auto inter) {
+  dispatch<4>(a, vec, [&](auto t, auto v, auto inter) {
     hipLaunchKernelGGL((qk_rope_vjp_kernel<decltype(t), decltype(v)::value, decltype(inter)::value>), dim3(blocks),
                        dim3(kWaves * 64), 0, st, a, s.group, s.share);
   });
-  if (gamma_q_grad) launch_column_sum(blocks, a.D, a.part, gamma_q_grad, st);
-  if (gamma_k_grad) launch_column_sum(blocks, a.D, a.part + (size_t)blocks * a.D, gamma_k_grad, st);
+  launch_column_sum(blocks, a.D, a.part, gamma_q_grad, gamma_k_grad, st);
 }
 
 }  // namespace fc

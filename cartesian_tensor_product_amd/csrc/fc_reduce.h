@@ -10,8 +10,9 @@ namespace fc {
 void launch_block_sum(int nblk, int n, const float* part, float* out, hipStream_t st);
 
 // The same sum for few columns and many blocks: 64 rows of part at a time,
-// then a tree over them; a fixed order as well, but another one.
-void launch_column_sum(int nblk, int n, const float* part, float* out, hipStream_t st);
+// then a tree over them; a fixed order as well, but another one.  out1 gets the
+// sums of a second array behind the first; either output may be absent.
+void launch_column_sum(int nblk, int n, const float* part, float* out, float* out1, hipStream_t st);
 
 // dst[i] += src[i] for i < n.
 void launch_add(size_t n, const float* src, float* dst, hipStream_t st);

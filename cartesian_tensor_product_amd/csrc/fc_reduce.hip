@@ -40,10 +40,13 @@ void launch_block_sum(int nblk, int n, const float* part, float* out, hipStream_
 
 // A block of 1024 threads covers 16 columns, thread (r, c) adds rows r, r + 64,
 // ... of column c.  With 1024 blocks of 128 values it takes 5 us where the
-// four waves per 64 columns above take 18 us.
+// four waves per 64 columns above take 18 us.  blockIdx.y: which of two arrays.
 __global__ __launch_bounds__(1024) void column_sum_kernel(int nblk, int n, const float* __restrict__ part,
-                                                          float* __restrict__ out) {
+                                                          float* __restrict__ out0, float* __restrict__ out1) {
   __shared__ float red[64][17];
+  float* out = blockIdx.y == 0 ? out0 : out1;
+  if (!out) return;
+  part += (size_t)blockIdx.y * nblk * n;
   const int c = threadIdx.x % 16, r = threadIdx.x / 16, i = blockIdx.x * 16 + c;
   float t = 0.f;
   if (i < n)
@@ -58,9 +61,9 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(int nblk, int n, const
   if (r == 0 && i < n) out[i] = red[0][c];
 }
 
-void launch_column_sum(int nblk, int n, const float* part, float* out, hipStream_t st) {
-  if (n <= 0) return;
-  hipLaunchKernelGGL(column_sum_kernel, dim3((n + 15) / 16), dim3(1024), 0, st, nblk, n, part, out);
+void launch_column_sum(int nblk, int n, const float* part, float* out, float* out1, hipStream_t st) {
+  if (n <= 0 || (!out && !out1)) return;
+  hipLaunchKernelGGL(column_sum_kernel, dim3((n + 15) / 16, out1 ? 2 : 1), dim3(1024), 0, st, nblk, n, part, out, out1);
 }
 
 __global__ __launch_bounds__(256) void add_kernel(size_t n, const float* __restrict__ src, float* __restrict__ dst) {
