@@ -103,9 +103,46 @@ __global__ __launch_bounds__(256) void sort_scan_kernel(int nblk, int* __restric
   for (int r = blockIdx.x * 256 + t; r < R; r += gridDim.x * 256) first[r] = last[r] = 0;
 }
 
-// Stable scatter: a wave takes 64 neighbouring keys at a time, finds the
-// lanes with its digit by one ballot per bit, and counts on from its own
-// earlier keys; waves and blocks follow in order.
+// Rank of the lane's digit d (bits wide; lanes out of `in` have none) among the
+// keys that the wave has seen: those counted in cnt, and those of lower lanes,
+// found by one ballot per bit.  Counts them.
+__device__ __forceinline__ int rank_of(int d, bool in, int bits, int lane, int* cnt) {
+  unsigned long long peers = __ballot(in);
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (d >> b) & 1;
+    const unsigned long long m = __ballot(in && set);
+    peers &= set ? m : ~m;
+  }
+  const int rank = in ? cnt[d] + __popcll(peers & ((1ull << lane) - 1)) : 0;
+  // every lane has read its count before the last peer adds the group
+  // (a wave's LDS accesses are served in order; the fences hold the compiler)
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (in && (peers >> lane) == 1ull) cnt[d] = rank + 1;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  return rank;
+}
+
+// Sum over the lower lanes of the 256 threads' values v (all threads of the
+// block call it; those from 256 on add nothing)
+__device__ __forceinline__ int sum_before(int v, int t, int* sums) {
+  const int lane = t % 64, w = t / 64;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 63 && w < 4) sums[w] = s;
+  __syncthreads();
+  int run = s - v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < w) run += sums[i];
+  return run;
+}
+
+// Stable scatter: a wave takes 64 neighbouring keys at a time
+// and counts on from its own earlier keys; waves and blocks follow in order.
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(int N, int R, int shift, int bits, bool first_pass,
                                                                     const int* __restrict__ keys,
                                                                     const int* __restrict__ ord,
@@ -131,37 +168,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(int N, int R
 #pragma unroll
   for (int i = 0; i < kSortRounds; ++i) {
     const bool in = base + i * 64 + lane < N;
-    const int d = (key[i] >> shift) & (ndig - 1);
-    unsigned long long peers = __ballot(in);
-    for (int b = 0; b < bits; ++b) {
-      const bool set = (d >> b) & 1;
-      const unsigned long long m = __ballot(in && set);
-      peers &= set ? m : ~m;
-    }
-    const int below = __popcll(peers & ((1ull << lane) - 1));
-    rank[i] = in ? cnt[w][d] + below : 0;
-    // every lane has read its count before the last peer adds the group
-    // (a wave's LDS accesses are served in order; the fences hold the compiler)
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (in && (peers >> lane) == 1ull) cnt[w][d] = rank[i] + 1;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    rank[i] = rank_of((key[i] >> shift) & (ndig - 1), in, bits, lane, cnt[w]);
   }
   __syncthreads();
   {  // digit t: first position = digits before + blocks before + waves before
-    const int v = digits;
-    int s = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(s, o);
-      if (lane >= o) s += u;
-    }
-    if (lane == 63) sums[w] = s;
-    __syncthreads();
-    int run = s - v;
-#pragma unroll
-    for (int i = 0; i < kSortWaves; ++i)
-      if (i < w) run += sums[i];
-    run += before;
+    int run = sum_before(digits, t, sums) + before;
 #pragma unroll
     for (int i = 0; i < kSortWaves; ++i) {
       const int c = cnt[i][t];
@@ -178,6 +189,61 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(int N, int R
     keys_out[p] = key[i];
     ord_out[p] = first_pass ? n : ord[n];
   }
+}
+
+// The whole sort of at most kSmall ids in one block, in LDS; the other blocks
+// clear the run bounds.  Three launches in all instead of five or eight (lookup
+// and gradient over 5000 rows of 128 channels: 4096 tokens 35 us, 4097 tokens,
+// sorted by the kernels above, 46 us).
+constexpr int kSmall = 4096, kSmallThreads = 1024;
+__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(int N, int R, int bits, int passes,
+                                                                   const int* __restrict__ ids,
+                                                                   int* __restrict__ keys_out,
+                                                                   int* __restrict__ ord_out, int* __restrict__ first,
+                                                                   int* __restrict__ last) {
+  constexpr int W = kSmallThreads / 64, ROUNDS = kSmall / kSmallThreads;
+  __shared__ int key[2][kSmall], ord[2][kSmall], cnt[W][256], sums[4];
+  const int t = threadIdx.x, lane = t % 64, w = t / 64, ndig = 1 << bits;
+  if (blockIdx.x > 0) {
+    for (int r = (blockIdx.x - 1) * kSmallThreads + t; r < R; r += (gridDim.x - 1) * kSmallThreads)
+      first[r] = last[r] = 0;
+    return;
+  }
+  for (int n = t; n < N; n += kSmallThreads) key[0][n] = key_of(ids[n], R), ord[0][n] = n;
+  for (int s = 0; s < passes; ++s) {
+    const int *k = key[s & 1], *o = ord[s & 1], shift = s * bits;
+    for (int i = t; i < W * 256; i += kSmallThreads) cnt[i / 256][i % 256] = 0;
+    __syncthreads();
+    const int base = w * (kSmall / W) + lane;
+    int rank[ROUNDS];
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int n = base + i * 64;
+      rank[i] = rank_of((k[min(n, N - 1)] >> shift) & (ndig - 1), n < N, bits, lane, cnt[w]);
+    }
+    __syncthreads();
+    int all = 0;
+    if (t < 256)
+      for (int i = 0; i < W; ++i) all += cnt[i][t];
+    int run = sum_before(all, t, sums);
+    if (t < 256)
+      for (int i = 0; i < W; ++i) {
+        const int c = cnt[i][t];
+        cnt[i][t] = run;
+        run += c;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int n = base + i * 64;
+      if (n >= N) continue;
+      const int p = cnt[w][(k[n] >> shift) & (ndig - 1)] + rank[i];
+      key[(s + 1) & 1][p] = k[n];
+      ord[(s + 1) & 1][p] = o[n];
+    }
+    __syncthreads();
+  }
+  for (int n = t; n < N; n += kSmallThreads) keys_out[n] = key[passes & 1][n], ord_out[n] = ord[passes & 1][n];
 }
 
 // ---------------------------------------------------------------- the sums --
@@ -265,14 +331,15 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(int N, int R, int C, int
 }
 
 // Rows whose run is cut by chunk edges, and rows without a token.  A wave
-// takes RW rows, whose bounds it reads at once.  The rows of a block lie a
-// grid apart, so that neighbouring frequent rows (tables are often ordered by
-// frequency) fall to different blocks.  Rows of more than kLong pieces
-// are left to the whole block, whose waves take pieces in turn and add up in
-// wave order.  gridDim.y blocks share the channels.
+// takes RW rows, 64 / group of them side by side (lookup and gradient of 49
+// tokens over 47725 rows of 24 channels: 31 us; 50 us with one row at a time).
+// The rows of a block lie a grid apart, so that neighbouring frequent rows
+// (tables are often ordered by frequency) fall to different blocks.  Rows of
+// more than kLong pieces are left to the whole block, whose waves take pieces in
+// turn and add up in wave order.  gridDim.y blocks share the channels.
 constexpr int kLong = 16;
 template <int W, int RW, int V>
-__global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int chunk, float scale,
+__global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int chunk, int group, float scale,
                                                             const int* __restrict__ first,
                                                             const int* __restrict__ last,
                                                             const float* __restrict__ part, float* __restrict__ grad) {
@@ -281,20 +348,22 @@ __global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int ch
   __shared__ float sum[W][64 * V];
   __shared__ int bound[2][ROWS];
   const int w = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const int c_begin = blockIdx.y * 64 * V, c_step = gridDim.y * 64 * V;
   auto row = [&](int i) { return (int)(blockIdx.x + i * gridDim.x); };
   const int rows = (R - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // at most ROWS
-  for (int i = threadIdx.x; i < rows; i += W * 64) bound[0][i] = first[row(i)], bound[1][i] = last[row(i)];
-  __syncthreads();
+  auto is_long = [&](int f, int l) { return l > f && (l - 1) / chunk - f / chunk >= kLong; };
+  bool own_long = false;
+  if (threadIdx.x < rows) {
+    const int f = first[row(threadIdx.x)], l = last[row(threadIdx.x)];
+    bound[0][threadIdx.x] = f, bound[1][threadIdx.x] = l;
+    own_long = is_long(f, l);
+  }
+  const bool any_long = __syncthreads_or(own_long);
   // piece of the run of chunks a..b: slot 1 of a unless the run begins there
   auto slot = [&](int f, int ch) { return part + ((size_t)ch * 2 + (ch * chunk < f ? 1 : 0)) * C; };
-  bool any_long = false;
-  for (int i = 0; i < rows; ++i) {
+  for (int i = w * RW + lane / group; i < min(rows, (w + 1) * RW); i += 64 / group) {
     const int f = bound[0][i], l = bound[1][i], a = f / chunk, b = (l - 1) / chunk;
-    const bool is_long = l > f && b - a >= kLong;
-    any_long |= is_long;
-    if (i / (RW == 1 ? W : RW) != w || is_long || (l > f && a == b)) continue;
-    for (int c = c_begin + lane * V; c < C; c += c_step) {
+    if (is_long(f, l) || (l > f && a == b)) continue;
+    for (int c = (blockIdx.y * group + lane % group) * V; c < C; c += gridDim.y * group * V) {
       float acc[V] = {};
       for (int ch = a; l > f && ch <= b; ++ch) {
         float x[V];
@@ -311,7 +380,7 @@ __global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int ch
   for (int i = 0; i < rows; ++i) {
     const int f = bound[0][i], l = bound[1][i], a = f / chunk, b = (l - 1) / chunk;
     if (l <= f || b - a < kLong) continue;
-    for (int c0 = c_begin; c0 < C; c0 += c_step) {
+    for (int c0 = blockIdx.y * 64 * V; c0 < C; c0 += gridDim.y * 64 * V) {
       const int c = c0 + lane * V;
       float acc[V] = {};
       if (c < C) {
@@ -384,9 +453,10 @@ void sum_t(const EmbedPlan& p, float scale, const int* key, const int* ord, cons
 template <int W, int RW, int V>
 void join_t(const EmbedPlan& p, float scale, float* grad, hipStream_t st) {
   constexpr int rows = RW == 1 ? 1 : W * RW;
-  const int y = RW == 1 ? (p.C + 64 * V - 1) / (64 * V) : 1;
+  const int pieces = (p.C + V - 1) / V, group = std::min(64, pow2_at_least(pieces));
+  const int y = RW == 1 ? (pieces + 63) / 64 : 1;
   hipLaunchKernelGGL((embed_join_kernel<W, RW, V>), dim3((p.R + rows - 1) / rows, y), dim3(W * 64), 0, st, p.R, p.C,
-                     p.chunk, scale, p.first, p.last, p.part, grad);
+                     p.chunk, group, scale, p.first, p.last, p.part, grad);
 }
 
 }  // namespace
@@ -440,7 +510,14 @@ void launch_embed_vjp(const EmbedPlan& p, bool is_bf16, float scale, const int* 
   const int ndig = 1 << p.bits;
   const int* key = ids;
   const int* ord = nullptr;
-  for (int s = 0; s < p.passes; ++s) {
+  const bool small = p.N <= kSmall;
+  if (small) {
+    hipLaunchKernelGGL(sort_small_kernel, dim3(1 + std::clamp(p.R / (4 * kSmallThreads), 1, 128)), dim3(kSmallThreads), 0,
+                       st, p.N, p.R, p.bits, p.passes, ids, p.key[0], p.ord[0], p.first, p.last);
+    key = p.key[0];
+    ord = p.ord[0];
+  }
+  for (int s = 0; s < (small ? 0 : p.passes); ++s) {
     int *ko = p.key[s & 1], *oo = p.ord[s & 1];
     hipLaunchKernelGGL(sort_count_kernel, dim3(p.sort_blocks), dim3(kSortThreads), 0, st, p.N, p.R, s * p.bits, ndig,
                        s == 0, key, p.hist);

@@ -65,17 +65,19 @@ def check(fc, d, table, ids, g):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("N,R,C", [(1, 1, 1), (1, 95, 128), (33, 7, 8), (257, 255, 5), (1000, 256, 128),
-                                   (2049, 300, 100), (5000, 70000, 24), (4096, 3, 1024), (300, 5, 2056)])
+                                   (2049, 300, 100), (5000, 70000, 24), (4096, 3, 1024), (300, 5, 2056),
+                                   (4095, 60000, 5), (4096, 255, 2), (4097, 256, 12), (9000, 300, 6)])
 def test_sizes(dtype, N, R, C):
     check(*case(dtype, N, R, C, N + R + C))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("ids", ["one", "sorted", "reversed", "padding", "last"])
-def test_orders_of_ids(dtype, ids):
+@pytest.mark.parametrize("N", [3001, 9001])
+def test_orders_of_ids(dtype, N, ids):
     """One row for every token (a run over many chunks), sorted and reversed
     ids, nothing but padding, the last row alone."""
-    N, R = 3001, 40
+    R = 40
     i = {"one": np.full(N, 17), "sorted": np.arange(N) * R // N, "reversed": R - 1 - np.arange(N) * R // N,
          "padding": np.where(np.arange(N) % 2, -1, R), "last": np.full(N, R - 1)}[ids]
     check(*case(dtype, N, R, 36, 3, ids=i))
