@@ -373,14 +373,40 @@ __device__ __forceinline__ Work find_work(const AttnArgs& a, int cols, int hb, i
     t = b / units;
   }
   if (t >= tiles || unit >= units) return w;
-  if (!KEYS) t = tiles - 1 - t;   // causal: the long columns (late queries, early keys) come first
   w.head = unit % heads * hb;
   w.split = unit / heads;
   auto clamp = [](int x, int l, int h) { return min(max(x, l), h); };
   const int* off = KEYS ? a.seg_k : a.seg_q;
   const int n = KEYS ? a.nk : a.nq, mul = KEYS ? 1 : a.G, lane = threadIdx.x % 64;
+  const int* other = KEYS ? a.seg_q : a.seg_k;
+  const int no = KEYS ? a.nq : a.nk;
   int seg = 0, c0 = 0, c1 = n;
-  if (off) {
+  // Of a causal segment the columns with long walks (late queries, early keys)
+  // come first.  Where not all blocks run at once, so do the segments with long
+  // walks, of up to 16: a long block that starts last would be waited for (7
+  // segments of 300 .. 2500 rows, 16 / 4 heads of 128, forward and VJP: 447 us in
+  // the segments' order, 408 us).  Sorting them costs half a microsecond.
+  if (off && a.S > 1 && a.S <= 16 && tiles * units > 256) {
+    const int s = min(lane, a.S - 1);
+    const int o0 = clamp(off[s], 0, n), o1 = clamp(off[s + 1], o0, n);
+    const int mine = lane < a.S ? (int)(((int64_t)(o1 - o0) * mul + cols - 1) / cols) : 0;
+    int walk = o1 - o0;
+    if (other != off) {
+      const int p0 = other ? clamp(other[s], 0, no) : 0;
+      walk = other ? clamp(other[s + 1], p0, no) - p0 : no;
+    }
+    int start = 0;
+    for (int k = 0; k < a.S; ++k) {
+      const int wk = __builtin_amdgcn_readlane(walk, k), tk = __builtin_amdgcn_readlane(mine, k);
+      start += wk > walk || (wk == walk && k < lane) ? tk : 0;
+    }
+    const unsigned long long here = __ballot(t >= start && t - start < mine);
+    seg = uniform(here == 0 ? 0 : __builtin_ctzll(here));
+    w.tile = here == 0 ? -1 : __builtin_amdgcn_readlane(KEYS ? t - start : mine - 1 - (t - start), seg);
+    c0 = __builtin_amdgcn_readlane(o0, seg);
+    c1 = __builtin_amdgcn_readlane(o1, seg);
+  } else if (off) {
+    if (!KEYS) t = tiles - 1 - t;
     int lo = 0, hi = a.S;
     while (hi - lo > 63) {   // 64 candidates per step
       const int step = (hi - lo + 63) / 64, s = lo + lane * step;
@@ -398,10 +424,8 @@ __device__ __forceinline__ Work find_work(const AttnArgs& a, int cols, int hb, i
     c0 = clamp(o0, 0, n);
     c1 = clamp(o1, c0, n);
   } else {
-    w.tile = t;
+    w.tile = KEYS ? t : tiles - 1 - t;
   }
-  const int* other = KEYS ? a.seg_q : a.seg_k;
-  const int no = KEYS ? a.nq : a.nk;
   int r0 = c0, r1 = c1;
   if (other != off) {
     r0 = other ? clamp(other[seg], 0, no) : 0;

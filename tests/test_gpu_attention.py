@@ -226,6 +226,14 @@ def test_few_keys_under_many_queries(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens_q,lens_k", [((40, 700, 0, 300, 1, 500, 33), None), ((300, 0, 500, 129, 129), (5, 60, 200, 0, 900))])
+def test_segments_of_different_lengths(dtype, causal, lens_q, lens_k):
+    """More blocks than run at once: the long segments are started first."""
+    Case(dtype, lens_q, lens_k, hq=16, hk=16, D=16, causal=causal, bias=not causal).check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("cap", [0.0, 20.0])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("lens_q,lens_k,causal", [((1, 1), None, True), ((5, 0, 1, 70), (1, 1, 1, 1), False), ((300,), (1,), False)])
