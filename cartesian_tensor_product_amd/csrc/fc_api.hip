@@ -33,8 +33,10 @@ static __device__ __align__(256) unsigned char scratch[kNoAllocScratchBytes];
 namespace {
 
 // bounds of the embedding, query/key norm and attention calls: what their
-// kernels count in 32 bits stays below 2^31
+// kernels count in 32 bits stays below 2^31, the threads of a launch below 2^32
 constexpr int kMaxRows = 1 << 30;
+constexpr int kMaxTable = 1 << 28;
+constexpr int kMaxNodes = 1 << 25;
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxStride = 1 << 22;
 
@@ -294,8 +296,9 @@ fc_status check_embed(const fc_embed_desc* d) {
   if (d->n_tokens < 0) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: n_tokens must be >= 0 (got %d)", d->n_tokens);
   if (d->n_rows < 1) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: n_rows must be >= 1 (got %d)", d->n_rows);
   if (d->channels < 1) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: channels must be >= 1 (got %d)", d->channels);
-  if (d->n_tokens > kMaxRows || d->n_rows > kMaxRows || d->channels > kMaxRows)
-    return fail(FC_ERR_UNSUPPORTED, "embedding: counts above %d are not supported", kMaxRows);
+  if (d->n_tokens > kMaxRows || d->n_rows > kMaxTable || d->channels > kMaxTable)
+    return fail(FC_ERR_UNSUPPORTED, "embedding: more than %d tokens or %d rows or channels are not supported", kMaxRows,
+                kMaxTable);
   if (!std::isfinite(d->scale)) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: scale must be finite");
   return check_dtype("embedding", d->dtype);
 }
@@ -309,9 +312,9 @@ fc_status check_qk(const fc_qk_rope_desc* d) {
     return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: head_dim must be even and >= 2 (got %d)", d->head_dim);
   if (d->head_dim > fc::kQkMaxDim)
     return fail(FC_ERR_UNSUPPORTED, "query/key norm: head_dim above %d is not supported", fc::kQkMaxDim);
-  if (d->heads_q > kMaxHeads || d->heads_k > kMaxHeads || d->n_nodes > kMaxRows)
+  if (d->heads_q > kMaxHeads || d->heads_k > kMaxHeads || d->n_nodes > kMaxNodes)
     return fail(FC_ERR_UNSUPPORTED, "query/key norm: more than %d heads or %d nodes are not supported", kMaxHeads,
-                kMaxRows);
+                kMaxNodes);
   if (d->n_freq < 0 || d->n_freq > d->head_dim / 2)
     return fail(FC_ERR_INVALID_ARGUMENT, "query/key norm: n_freq must be in [0, head_dim / 2] (got %d)", d->n_freq);
   if (d->q_stride != 0 && d->q_stride < d->heads_q * d->head_dim)
@@ -374,8 +377,8 @@ fc_status check_attn(const fc_attn_desc* d) {
   // of a launch too
   const int64_t packed = (int64_t)d->n_query * (d->heads_q / d->heads_k);
   if (packed > kMaxRows || d->n_key > kMaxRows || d->n_segments > kMaxRows / 64 ||
-      (std::max<int64_t>(packed, d->n_key) / 32 + d->n_segments) * d->heads_k > (int64_t(1) << 28))
-    return fail(FC_ERR_UNSUPPORTED, "attention: too many rows (n_query heads_q / heads_k and n_key up to %d)", kMaxRows);
+      (std::max<int64_t>(packed, d->n_key) / 32 + d->n_segments) * d->heads_k > (int64_t(1) << 24))
+    return fail(FC_ERR_UNSUPPORTED, "attention: too many rows (n_query heads_q and n_key heads_k up to 2^29)");
   const int piece = d->dtype == FC_BF16 ? 8 : 4;
   const int rows[3] = {d->heads_q * d->head_dim, d->heads_k * d->head_dim, d->heads_k * d->head_dim};
   const int32_t strides[3] = {d->q_stride, d->k_stride, d->v_stride};

@@ -123,7 +123,7 @@ struct PassPlan {
 //    traffic.
 //  * Else four waves share the walk (kRows: four times the blocks; one segment
 //    of 939 rows, one head of 64 in fp32, forward and VJP: 269 us as kCols with
-//    8 blocks against 109 us), also split in parts of 256 rows.
+//    8 blocks in one part against 70 us), also split in parts of 256 rows.
 //  * Short walks (molecules): waves go alone (kOne).
 //  * The key pass of wide bfloat16 heads (one wave per SIMD for its registers)
 //    takes kRows also with many columns: with one wave, waiting for the three

@@ -29,6 +29,20 @@
 // cycles during which no vector instruction issues, 592 for a depth of 16; six
 // bfloat16 ones take 222 and vector work goes on meanwhile.
 //
+// Bound by the vector units, which form the scores' tanh, distance, exponential
+// and parts, and by latency where registers leave one or two waves per SIMD.
+// Measured, forward / query pass / key pass:
+//   4096 rows, 4 heads of 32, fp32, slopes: 77 / 120 / 150 us (vector units 58 %
+//   busy, matrix units 30 %; 30 GFLOP in 328 us with the joins, 92 TFLOP/s; the
+//   fp32 matrix product of the library runs at 151);
+//   384 molecules of 5 .. 120 atoms, 8 heads of 16, fp32, slopes: 46 / 60 / 77 us
+//   (vector units 40 .. 50 % busy);
+//   7 packed causal segments of 300 .. 2500 rows, 16 / 4 heads of 128, bfloat16,
+//   cap: 90 / 125 / 249 us (matrix units 21 / 23 / 15 % busy; the key pass has one
+//   wave per SIMD, which nothing covers);
+//   16384 rows, 8 heads of 64, bfloat16, slopes, forward: 1.00 ms, 549 TFLOP/s
+//   (vector units 60 % busy, two waves per SIMD).
+//
 // No atomics: each output has one writer, and the VJP is two passes, which
 // repeats the scores (seven products instead of five) but keeps results
 // bitwise reproducible.
@@ -550,14 +564,18 @@ __device__ __forceinline__ void join_values(float* buf, float (&v)[N]) {
 
 // Waves per SIMD that a kernel's registers allow: columns and accumulators of
 // all heads, `live` 32x32 results at a time, the tile on its way, and what
-// goes into addresses, scalars and reads ahead from LDS, out of 512.
+// goes into addresses, scalars and reads ahead from LDS, out of 512; and that
+// the row tiles of their blocks allow, out of 160 KB of LDS.
 template <class T, int DP, int HB, int MODE, bool BIAS>
 constexpr int waves_per_simd(int frags, int accs, int live, int rows) {
   using TL = Tile<T, DP, HB>;
   const int regs = frags * HB * TL::STEPS * TL::NP * 4 + accs * HB * TL::DB * 16 + live * 16 +
                    2 * 4 * ((rows * TL::CPR + Waves<MODE>::STAGE - 1) / Waves<MODE>::STAGE) + (BIAS ? 100 : 60) +
                    (accs == 2 && TL::NP == 3 ? 40 : 0);
-  return regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+  constexpr int lds = Waves<MODE>::REGIONS * (2 * TL::LD * TL::NP * 2 + (BIAS ? 32 : 16));   // of a tile row
+  const int room = (163840 / (lds * rows) * Waves<MODE>::NW + 3) / 4;
+  const int waves = regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+  return waves < room ? waves : room > 0 ? room : 1;
 }
 
 // ---------------------------------------------------------------- forward --

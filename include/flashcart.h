@@ -493,8 +493,8 @@ typedef int32_t fc_dtype;
  *   out[n][c] = scale * table[ids[n]][c]
  * table [n_rows][channels] and out [n_tokens][channels] have the element type
  * `dtype`; ids int32 [n_tokens].  An id outside [0, n_rows) is padding: its
- * output row is zero and it adds nothing to the gradient.  n_tokens >= 0,
- * n_rows >= 1, channels >= 1, scale finite.  16-byte pieces are used where
+ * output row is zero and it adds nothing to the gradient.  n_tokens >= 0 (up
+ * to 2^30), n_rows >= 1 and channels >= 1 (up to 2^28), scale finite.  16-byte pieces are used where
  * channels and pointers allow them; other sizes work element by element.
  * ---------------------------------------------------------------------- */
 typedef struct {
@@ -530,8 +530,8 @@ fc_status fc_embed_vjp(const fc_embed_desc* d, const int32_t* ids, const void* g
  * output; q_out, k_out and every gradient are packed.  gamma_q, gamma_k: fp32
  * [head_dim], NULL for ones; pos, freq: fp32, both NULL for no rotation.
  * heads_k = 0 (k, k_out NULL) treats the queries alone (gamma_k_grad is then
- * zero).  n_nodes >= 0,
- * heads_q >= 1, head_dim even and <= 128, 0 <= n_freq <= head_dim / 2, eps > 0.
+ * zero).  n_nodes >= 0 (up to 2^25),
+ * heads_q >= 1 (up to 1024), head_dim even and <= 128, 0 <= n_freq <= head_dim / 2, eps > 0.
  * ---------------------------------------------------------------------- */
 #define FC_ROPE_INTERLEAVED 1u
 
@@ -578,16 +578,17 @@ fc_status fc_qk_norm_rope_vjp(const fc_qk_rope_desc* d, const void* q, const voi
  * keys are the queries' atoms (n_key = n_query, segments->k NULL).
  * Distances are between the given points (no periodic images); their
  * gradient is 0 at distance 0.
- * Requirements: n_query, n_key >= 0, n_segments >= 1, heads_k >= 1,
+ * Requirements: n_query, n_key >= 0 (n_query heads_q and n_key heads_k up to
+ * 2^29), n_segments >= 1, heads_k >= 1,
  * heads_q <= 256 a multiple of heads_k, head_dim a multiple of 8 and <= 128,
  * scale > 0, cap >= 0; q, k, v, out, g_out and their gradients 16-byte
  * aligned with strides of whole 16-byte pieces, at most 2^22 elements.
  * Values inside a segment must be finite, also those a causal mask hides;
  * rows behind the last segment may hold anything: they are not read, and
  * their outputs and gradients are left as they were.
- * In bfloat16 the probabilities and the score gradients are rounded to
- * bfloat16 as operands of the matrix cores; statistics and the position and
- * slope gradients stay in fp32.
+ * In bfloat16 the probabilities and the score gradients are rounded to one
+ * or two bfloat16 parts as operands of the matrix cores; statistics and the
+ * position and slope gradients stay in fp32.
  * Few queries over many keys (and the reverse) are split over the long axis;
  * the workspace holds the parts.  Calls that may run at the same time (two
  * streams, two graphs) need a workspace each.

@@ -20,6 +20,8 @@ def raises(status, f, *args, **kw):
     (dict(n_rows=0), fc.FC_ERR_INVALID_ARGUMENT),
     (dict(channels=0), fc.FC_ERR_INVALID_ARGUMENT),
     (dict(n_rows=2 ** 31 - 1), fc.FC_ERR_UNSUPPORTED),
+    (dict(n_rows=2 ** 28 + 1), fc.FC_ERR_UNSUPPORTED),    # more threads than a launch may have
+    (dict(n_tokens=2 ** 30 + 1), fc.FC_ERR_UNSUPPORTED),
     (dict(scale=float("nan")), fc.FC_ERR_INVALID_ARGUMENT),
     (dict(dtype=2), fc.FC_ERR_UNSUPPORTED),
     (dict(), fc.FC_ERR_INVALID_ARGUMENT),                 # NULL arrays
@@ -44,6 +46,7 @@ def test_embed_refusals(bad, status):
     (dict(flags=2), fc.FC_ERR_UNSUPPORTED),
     (dict(dtype=-1), fc.FC_ERR_UNSUPPORTED),
     (dict(heads_q=2000), fc.FC_ERR_UNSUPPORTED),
+    (dict(n_nodes=2 ** 25 + 1), fc.FC_ERR_UNSUPPORTED),
     (dict(), fc.FC_ERR_INVALID_ARGUMENT),                 # NULL arrays
 ])
 def test_qk_norm_rope_refusals(bad, status):
@@ -69,6 +72,7 @@ def test_qk_norm_rope_refusals(bad, status):
     (dict(flags=4), fc.FC_ERR_UNSUPPORTED),
     (dict(dtype=3), fc.FC_ERR_UNSUPPORTED),
     (dict(n_query=2 ** 30, n_key=2 ** 30), fc.FC_ERR_UNSUPPORTED),
+    (dict(n_query=2 ** 28, n_key=2 ** 29), fc.FC_ERR_UNSUPPORTED),
     (dict(), fc.FC_ERR_INVALID_ARGUMENT),                 # NULL arrays
 ])
 def test_attention_refusals(bad, status):
