@@ -38,8 +38,8 @@
 //   384 molecules of 5 .. 120 atoms, 8 heads of 16, fp32, slopes: 46 / 60 / 77 us
 //   (vector units 40 .. 50 % busy);
 //   7 packed causal segments of 300 .. 2500 rows, 16 / 4 heads of 128, bfloat16,
-//   cap: 90 / 125 / 249 us (matrix units 21 / 23 / 15 % busy; the key pass has one
-//   wave per SIMD, which nothing covers);
+//   cap: 86 / 119 / 224 us (matrix units 22 / 24 / 17 % busy; the key pass has one
+//   wave per SIMD, whose waits nothing covers);
 //   16384 rows, 8 heads of 64, bfloat16, slopes, forward: 1.00 ms, 549 TFLOP/s
 //   (vector units 60 % busy, two waves per SIMD).
 //
