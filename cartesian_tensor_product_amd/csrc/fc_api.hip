@@ -36,6 +36,7 @@ namespace {
 // kernels count in 32 bits stays below 2^31, the threads of a launch below 2^32
 constexpr int kMaxRows = 1 << 30;
 constexpr int kMaxTable = 1 << 28;
+constexpr int kMaxChannels = 1 << 21;
 constexpr int kMaxNodes = 1 << 25;
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxStride = 1 << 22;
@@ -296,9 +297,9 @@ fc_status check_embed(const fc_embed_desc* d) {
   if (d->n_tokens < 0) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: n_tokens must be >= 0 (got %d)", d->n_tokens);
   if (d->n_rows < 1) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: n_rows must be >= 1 (got %d)", d->n_rows);
   if (d->channels < 1) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: channels must be >= 1 (got %d)", d->channels);
-  if (d->n_tokens > kMaxRows || d->n_rows > kMaxTable || d->channels > kMaxTable)
-    return fail(FC_ERR_UNSUPPORTED, "embedding: more than %d tokens or %d rows or channels are not supported", kMaxRows,
-                kMaxTable);
+  if (d->n_tokens > kMaxRows || d->n_rows > kMaxTable || d->channels > kMaxChannels)
+    return fail(FC_ERR_UNSUPPORTED, "embedding: more than %d tokens, %d rows or %d channels are not supported", kMaxRows,
+                kMaxTable, kMaxChannels);
   if (!std::isfinite(d->scale)) return fail(FC_ERR_INVALID_ARGUMENT, "embedding: scale must be finite");
   return check_dtype("embedding", d->dtype);
 }

@@ -7,10 +7,12 @@
 
 namespace fc {
 
-// Workspace of the gradient: sorted keys and order (two buffers each),
-// digit counts, run bounds per row, partial sums of runs cut by a chunk edge.
+// Workspace of the gradient: sums of a few rows per window of tokens, or sorted
+// keys and order (two buffers each), digit counts, run bounds per row, partial
+// sums of runs cut by a chunk edge.
 struct EmbedPlan {
   int N, R, C;
+  int windows;           // of tokens, for tables of few rows; else 0
   int passes, bits;      // radix sort: digits of `bits` bits
   int sort_blocks;       // blocks of the sort's passes
   int chunk, chunks;     // sorted tokens per chunk of the sum, number of chunks

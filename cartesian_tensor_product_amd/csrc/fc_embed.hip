@@ -415,6 +415,119 @@ __global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int ch
   }
 }
 
+// ----------------------------------------------------------- tables of few rows --
+
+// A table of few rows (species): a block sorts a window of kWindow tokens in
+// LDS, sums the runs of that order and writes its sum of every row,
+// part[window][R][C]; the next kernel adds the windows in order.  Each group of
+// lanes walks `per` tokens; runs that go on over groups meet in LDS.  The rows of
+// g are read window by window, not over all tokens row by row.
+constexpr int kWindow = 1024, kFewRows = 128;
+template <class T, int V>
+__global__ __launch_bounds__(kWindow) void embed_window_kernel(int N, int R, int C, int group, int per,
+                                                               const int* __restrict__ ids, const T* __restrict__ g,
+                                                               float* __restrict__ part) {
+  constexpr int W = kWindow / 64;
+  __shared__ int cnt[W][256], start[256], sums[4], key[kWindow], ord[kWindow];
+  // sums of a group's first run where it began before (0), and of its last where
+  // it goes on (1)
+  __shared__ __align__(32) float edge[2][kWindow * V];
+  const int t = threadIdx.x, lane = t % 64, w = t / 64;
+  for (int i = t; i < W * 256; i += kWindow) cnt[i / 256][i % 256] = 0;
+  const int n = blockIdx.x * kWindow + t;
+  const int k = n < N ? key_of(ids[n], R) : R;   // below 256
+  __syncthreads();
+  const int rank = rank_of(k, true, 8, lane, cnt[w]);
+  __syncthreads();
+  int all = 0;
+  if (t < 256)
+    for (int i = 0; i < W; ++i) all += cnt[i][t];
+  int run = sum_before(all, t, sums);
+  if (t < 256) {
+    start[t] = run;
+    for (int i = 0; i < W; ++i) {
+      const int c = cnt[i][t];
+      cnt[i][t] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  const int place = cnt[w][k] + rank;
+  key[place] = k;
+  ord[place] = n;
+  __syncthreads();
+  const int real = start[R];   // padding is sorted last
+  const int gi = t / group, c = (blockIdx.y * group + t % group) * V;
+  const int p0 = gi * per, p1 = min(p0 + per, real);
+  const bool on = c < C;
+  float* out = part + (size_t)blockIdx.x * R * C + c;
+  float acc[V] = {};
+  int cur = 0;
+  bool goes_on = false;
+  if (p0 < p1 && on) {
+    cur = key[p0];
+    bool before = p0 > 0 && key[p0 - 1] == cur;
+    auto put = [&](float* dst) { store_f32<float, V>(dst, acc); };
+    constexpr int U = 16;
+    for (int p = p0; p < p1; p += U) {
+      Pack<T, V> x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[u] = *reinterpret_cast<const Pack<T, V>*>(g + (size_t)ord[min(p + u, p1 - 1)] * C + c);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (p + u >= p1) break;
+        const int next = key[p + u];
+        if (next != cur) {
+          put(before ? edge[0] + t * V : out + (size_t)cur * C);
+          before = false;
+          cur = next;
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += static_cast<float>(x[u].e[e]);
+      }
+    }
+    goes_on = p1 < real && key[p1] == cur;
+    put(before ? edge[0] + t * V : goes_on ? edge[1] + t * V : out + (size_t)cur * C);
+    goes_on &= !before;
+  }
+  __syncthreads();
+  if (goes_on) {
+    for (int h = gi + 1; h * per < real && key[h * per] == cur; ++h) {
+      float x[V];
+      load_f32<float, V>(edge[0] + (t + (h - gi) * group) * V, x);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += x[e];
+    }
+    store_f32<float, V>(out + (size_t)cur * C, acc);
+  }
+  if (!on) return;
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int r = gi; r < R; r += kWindow / group)
+    if (start[r] == start[r + 1]) store_f32<float, V>(out + (size_t)r * C, acc);
+}
+
+// grad[i] = scale sum_b part[b][i]: a block of 16 waves for 64 columns
+__global__ __launch_bounds__(1024) void embed_window_join_kernel(int windows, size_t n, float scale,
+                                                                 const float* __restrict__ part,
+                                                                 float* __restrict__ grad) {
+  __shared__ float sum[16][64];
+  const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
+  const size_t i = (size_t)blockIdx.x * 64 + lane;
+  float acc = 0.f;
+  if (i < n)
+#pragma unroll 8
+    for (int b = w; b < windows; b += 16) acc += part[b * n + i];
+  sum[w][lane] = acc;
+  __syncthreads();
+  if (w > 0 || i >= n) return;
+  for (int j = 1; j < 16; ++j) acc += sum[j][lane];
+  grad[i] = acc * scale;
+}
+
 int pow2_at_least(int n) {
   int p = 1;
   while (p < n) p <<= 1;
@@ -480,6 +593,12 @@ EmbedPlan embed_plan(int N, int R, int C, bool bf16, bool aligned, void* ws) {
   const int pieces = (C + p.vec - 1) / p.vec;
   p.group = std::min(64, pow2_at_least(pieces));
   p.slices = (pieces + p.group - 1) / p.group;
+  if (R <= kFewRows) {
+    p.windows = (N + kWindow - 1) / kWindow;
+    p.part = static_cast<float*>(ws);
+    p.bytes = sizeof(float) * (size_t)p.windows * R * C;
+    return p;
+  }
   // chunks of 32 tokens at least (the partial sums then stay below a
   // sixteenth of what is read), longer once 16 waves per CU have one each
   const long long groups = 256ll * 16 * (64 / p.group);
@@ -514,6 +633,18 @@ void launch_embed_fwd(int N, int R, int C, bool is_bf16, bool aligned, float sca
 
 void launch_embed_vjp(const EmbedPlan& p, bool is_bf16, float scale, const int* ids, const void* g, float* grad,
                       hipStream_t st) {
+  if (p.windows > 0) {
+    const int per = std::max(p.group, 16);   // the threads beyond kWindow / per groups only sort
+    dispatch(is_bf16, p.vec, [&](auto t, auto v) {
+      using E = decltype(t);
+      hipLaunchKernelGGL((embed_window_kernel<E, decltype(v)::value>), dim3(p.windows, p.slices), dim3(kWindow), 0, st,
+                         p.N, p.R, p.C, p.group, per, ids, static_cast<const E*>(g), p.part);
+    });
+    const size_t n = (size_t)p.R * p.C;
+    hipLaunchKernelGGL(embed_window_join_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, st, p.windows, n, scale,
+                       p.part, grad);
+    return;
+  }
   const int ndig = 1 << p.bits;
   const int* key = ids;
   const int* ord = nullptr;

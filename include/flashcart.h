@@ -494,7 +494,7 @@ typedef int32_t fc_dtype;
  * table [n_rows][channels] and out [n_tokens][channels] have the element type
  * `dtype`; ids int32 [n_tokens].  An id outside [0, n_rows) is padding: its
  * output row is zero and it adds nothing to the gradient.  n_tokens >= 0 (up
- * to 2^30), n_rows >= 1 and channels >= 1 (up to 2^28), scale finite.  16-byte pieces are used where
+ * to 2^30), n_rows >= 1 (up to 2^28), channels >= 1 (up to 2^21), scale finite.  16-byte pieces are used where
  * channels and pointers allow them; other sizes work element by element.
  * ---------------------------------------------------------------------- */
 typedef struct {
@@ -510,7 +510,7 @@ fc_status fc_embed_fwd(const fc_embed_desc* d, const void* table, const int32_t*
  * `dtype`), the sum over the tokens of each row in a fixed order (tokens
  * sorted by row), zero for rows without a token.  g_out [n_tokens][channels]
  * of type `dtype`.  Needs fc_embed_workspace_bytes(d) bytes (256-byte
- * aligned). */
+ * aligned), of its own where calls may run at the same time. */
 size_t fc_embed_workspace_bytes(const fc_embed_desc* d);
 fc_status fc_embed_vjp(const fc_embed_desc* d, const int32_t* ids, const void* g_out, float* table_grad,
                        void* workspace, size_t workspace_bytes, hipStream_t stream);
@@ -551,7 +551,8 @@ fc_status fc_qk_norm_rope_fwd(const fc_qk_rope_desc* d, const void* q, const voi
  * k_grad (type `dtype`), gamma_q_grad, gamma_k_grad (fp32 [head_dim], summed
  * over nodes and heads in a fixed order) and pos_grad (fp32 [n_nodes][3]),
  * each when non-NULL (at least one).  freq is a constant.  A gamma gradient
- * needs fc_qk_norm_rope_workspace_bytes(d) bytes. */
+ * needs fc_qk_norm_rope_workspace_bytes(d) bytes, of its own where calls may
+ * run at the same time. */
 size_t fc_qk_norm_rope_workspace_bytes(const fc_qk_rope_desc* d);
 fc_status fc_qk_norm_rope_vjp(const fc_qk_rope_desc* d, const void* q, const void* k,
                               const float* gamma_q, const float* gamma_k, const float* pos,

@@ -22,6 +22,7 @@ def raises(status, f, *args, **kw):
     (dict(n_rows=2 ** 31 - 1), fc.FC_ERR_UNSUPPORTED),
     (dict(n_rows=2 ** 28 + 1), fc.FC_ERR_UNSUPPORTED),    # more threads than a launch may have
     (dict(n_tokens=2 ** 30 + 1), fc.FC_ERR_UNSUPPORTED),
+    (dict(channels=2 ** 21 + 1), fc.FC_ERR_UNSUPPORTED),
     (dict(scale=float("nan")), fc.FC_ERR_INVALID_ARGUMENT),
     (dict(dtype=2), fc.FC_ERR_UNSUPPORTED),
     (dict(), fc.FC_ERR_INVALID_ARGUMENT),                 # NULL arrays

@@ -66,28 +66,29 @@ def check(fc, d, table, ids, g):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("N,R,C", [(1, 1, 1), (1, 95, 128), (33, 7, 8), (257, 255, 5), (1000, 256, 128),
                                    (2049, 300, 100), (5000, 70000, 24), (4096, 3, 1024), (300, 5, 2056),
-                                   (4095, 60000, 5), (4096, 255, 2), (4097, 256, 12), (9000, 300, 6)])
+                                   (4095, 60000, 5), (4096, 255, 2), (4097, 256, 12), (9000, 300, 6),
+                                   (5000, 128, 100), (5000, 129, 100), (3000, 64, 320), (2500, 2, 1)])
 def test_sizes(dtype, N, R, C):
     check(*case(dtype, N, R, C, N + R + C))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("ids", ["one", "sorted", "reversed", "padding", "last"])
-@pytest.mark.parametrize("N", [3001, 9001])
-def test_orders_of_ids(dtype, N, ids):
+@pytest.mark.parametrize("N,R", [(3001, 40), (3001, 200), (9001, 200)])
+def test_orders_of_ids(dtype, N, R, ids):
     """One row for every token (a run over many chunks), sorted and reversed
     ids, nothing but padding, the last row alone."""
-    R = 40
     i = {"one": np.full(N, 17), "sorted": np.arange(N) * R // N, "reversed": R - 1 - np.arange(N) * R // N,
          "padding": np.where(np.arange(N) % 2, -1, R), "last": np.full(N, R - 1)}[ids]
     check(*case(dtype, N, R, 36, 3, ids=i))
 
 
-def test_long_runs_and_many_chunks():
-    """More tokens than one pass of chunks: two rows of tens of thousands."""
+@pytest.mark.parametrize("R", [9, 150])
+def test_long_runs_and_many_chunks(R):
+    """More tokens than one pass of chunks: a row of tens of thousands."""
     rng = np.random.default_rng(9)
-    ids = np.where(rng.random(70000) < 0.5, 2, rng.integers(0, 9, 70000))
-    check(*case("f32", 70000, 9, 16, 4, ids=ids))
+    ids = np.where(rng.random(70000) < 0.5, 2, rng.integers(0, R, 70000))
+    check(*case("f32", 70000, R, 16, 4, ids=ids))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
