@@ -7,18 +7,23 @@
 // 95 rows of 128 in fp32: 28 us, 5.5 TB/s; one call of 1000 tokens 2.4 us).
 //
 // Gradient: sums over tokens of one row in a fixed order, without
-// floating-point atomics.  A stable radix sort of the ids gives the tokens of
-// each row as one run of the sorted order.  The order is cut into chunks of
-// equal length whatever the runs are, so that one very frequent row (a common
-// species) costs no more than many rare ones.  A group of lanes walks its
-// chunk, adds the tokens' rows in fp32 and writes a row when its run ends;
-// the runs cut by a chunk edge go to partial sums (at most two per chunk),
-// which the last kernel adds in chunk order.  That kernel also writes the
-// zeros of rows without a token.  Bound by the read of g, row by row in sorted
-// order: 300000 tokens, 95 rows of 128 in fp32 77 us, of which the sort takes 17,
-// the sums 51 (3.0 TB/s) and the join 9; 65536 tokens, 50000 rows of 512 in
-// bfloat16 82 us, of which two sorting passes take 32, the sums 30 and the join,
-// which writes most of the 102 MB table, 20 (5 TB/s).
+// floating-point atomics, from a stable sort of the ids.
+//  * Tables of up to 255 rows (species): a block sorts 1024 neighbouring tokens
+//    and sums them row by row; a second kernel adds up the blocks.  300000
+//    tokens, 95 rows of 128 in fp32: 51 and 5 us; bound by the read of g (3 TB/s)
+//    behind each block's own sort.
+//  * Larger ones: a radix sort of all ids gives the tokens of each row as one run
+//    of the sorted order, cut into chunks of equal length whatever the runs are,
+//    so that one very frequent row costs no more than many rare ones.  A group of
+//    lanes walks its chunk, adds the tokens' rows in fp32 and writes a row when
+//    its run ends; the runs cut by a chunk edge go to partial sums (at most two
+//    per chunk), which the last kernel adds in chunk order.  That kernel also
+//    writes the zeros of rows without a token.  65536 tokens, 50000 rows of 512 in
+//    bfloat16: two sorting passes 32 us, the sums 30 and the join, which writes
+//    most of the 102 MB table, 20 (5 TB/s).
+// Lookup and gradient with 255 rows and, all ids sorted, with 256: 300000 tokens
+// of 128 channels 94 and 115 us in fp32, 52 and 94 us in bfloat16; 4096 tokens 17
+// and 30 us.
 #include "fc_embed.h"
 
 #include <algorithm>
@@ -255,7 +260,8 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(int N, int R,
 
 // One group of `group` lanes per (chunk, channel slice); lane i of the group
 // holds V channels.  Shorter chunks (32 tokens for 64) leave its time as it is
-// and lengthen the join (9 to 13 us, 300000 tokens).  part[chunk][2][C]: the sum of the run that begins at or
+// and lengthen the join (9 to 13 us, 300000
+// tokens over 95 rows).  part[chunk][2][C]: the sum of the run that begins at or
 // before the chunk's first token and does not end inside it alone (slot 0),
 // and of the run that begins inside and continues behind the chunk (slot 1).
 template <class T, int V>
@@ -422,7 +428,7 @@ __global__ __launch_bounds__(W * 64) void embed_join_kernel(int R, int C, int ch
 // part[window][R][C]; the next kernel adds the windows in order.  Each group of
 // lanes walks `per` tokens; runs that go on over groups meet in LDS.  The rows of
 // g are read window by window, not over all tokens row by row.
-constexpr int kWindow = 1024, kFewRows = 128;
+constexpr int kWindow = 1024, kFewRows = 255;   // keys 0..255: one digit
 template <class T, int V>
 __global__ __launch_bounds__(kWindow) void embed_window_kernel(int N, int R, int C, int group, int per,
                                                                const int* __restrict__ ids, const T* __restrict__ g,

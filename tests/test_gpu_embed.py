@@ -67,14 +67,14 @@ def check(fc, d, table, ids, g):
 @pytest.mark.parametrize("N,R,C", [(1, 1, 1), (1, 95, 128), (33, 7, 8), (257, 255, 5), (1000, 256, 128),
                                    (2049, 300, 100), (5000, 70000, 24), (4096, 3, 1024), (300, 5, 2056),
                                    (4095, 60000, 5), (4096, 255, 2), (4097, 256, 12), (9000, 300, 6),
-                                   (5000, 128, 100), (5000, 129, 100), (3000, 64, 320), (2500, 2, 1)])
+                                   (5000, 128, 100), (5000, 129, 100), (3000, 64, 320), (2500, 2, 1), (5000, 255, 72)])
 def test_sizes(dtype, N, R, C):
     check(*case(dtype, N, R, C, N + R + C))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("ids", ["one", "sorted", "reversed", "padding", "last"])
-@pytest.mark.parametrize("N,R", [(3001, 40), (3001, 200), (9001, 200)])
+@pytest.mark.parametrize("N,R", [(3001, 40), (3001, 300), (9001, 300)])
 def test_orders_of_ids(dtype, N, R, ids):
     """One row for every token (a run over many chunks), sorted and reversed
     ids, nothing but padding, the last row alone."""
@@ -83,7 +83,7 @@ def test_orders_of_ids(dtype, N, R, ids):
     check(*case(dtype, N, R, 36, 3, ids=i))
 
 
-@pytest.mark.parametrize("R", [9, 150])
+@pytest.mark.parametrize("R", [9, 300])
 def test_long_runs_and_many_chunks(R):
     """More tokens than one pass of chunks: a row of tens of thousands."""
     rng = np.random.default_rng(9)
